@@ -9,6 +9,7 @@ built -- there is no CPU fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -40,7 +41,11 @@ EXPORTED = (
     "infini_attn_layer_forward", "infini_attn_layer_workspace_size", "infini_attn_decode_step",
     "infini_attn_workspace_size_ex", "infini_attn_gemm_bf16", "infini_attn_backward",
     "infini_attn_backward_workspace_size", "infini_attn_trim_workspace", "infini_attn_last_cuda_error",
+    "infini_attn_gated_delta_forward", "infini_attn_gated_delta_workspace_size", "infini_attn_gated_delta_step",
+    "infini_attn_gated_delta_params_size", "infini_attn_layer_norm_forward", "infini_attn_layer_norm_backward",
+    "infini_attn_layer_norm_backward_workspace_size",
 )
+WEIGHT_F32 = 0x20
 
 
 def _load():
@@ -130,6 +135,46 @@ lib.infini_attn_trim_workspace.argtypes = []
 lib.infini_attn_trim_workspace.restype = _i
 
 
+class GatedDeltaParams(ctypes.Structure):
+    """Mirror of ``infini_attn_gated_delta_params`` (include/infini_attn.h)."""
+
+    _fields_ = [
+        ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp), ("beta", _vp), ("S", _vp), ("out", _vp), ("lens", _vp),
+        ("B", _i), ("H", _i), ("Hk", _i), ("L", _ll), ("dk", _i), ("dv", _i), ("mode", _i), ("scale", ctypes.c_float),
+        ("q_stride", _ll * 3), ("k_stride", _ll * 3), ("v_stride", _ll * 3), ("o_stride", _ll * 3),
+        ("g_stride", _ll * 3), ("beta_stride", _ll * 3),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+class GatedDeltaStepParams(ctypes.Structure):
+    """Mirror of ``infini_attn_gated_delta_step_params`` (include/infini_attn.h)."""
+
+    _fields_ = [
+        ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp), ("beta", _vp), ("S", _vp), ("out", _vp), ("slots", _vp),
+        ("B", _i), ("H", _i), ("Hk", _i), ("pool", _ll), ("dk", _i), ("dv", _i), ("mode", _i),
+        ("scale", ctypes.c_float),
+        ("q_stride", _ll * 2), ("k_stride", _ll * 2), ("v_stride", _ll * 2), ("o_stride", _ll * 2),
+        ("g_stride", _ll * 2), ("beta_stride", _ll * 2), ("stream", _vp),
+    ]
+
+
+lib.infini_attn_gated_delta_forward.argtypes = [ctypes.POINTER(GatedDeltaParams)]
+lib.infini_attn_gated_delta_forward.restype = _i
+lib.infini_attn_gated_delta_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaParams)]
+lib.infini_attn_gated_delta_workspace_size.restype = ctypes.c_size_t
+lib.infini_attn_gated_delta_step.argtypes = [ctypes.POINTER(GatedDeltaStepParams)]
+lib.infini_attn_gated_delta_step.restype = _i
+lib.infini_attn_gated_delta_params_size.argtypes = [_i]
+lib.infini_attn_gated_delta_params_size.restype = ctypes.c_size_t
+lib.infini_attn_layer_norm_forward.argtypes = [_vp] * 4 + [_ll, _i, ctypes.c_float, _i, _vp]
+lib.infini_attn_layer_norm_forward.restype = _i
+lib.infini_attn_layer_norm_backward.argtypes = [_vp] * 6 + [_ll, _i, ctypes.c_float, _i, _vp, ctypes.c_size_t, _vp]
+lib.infini_attn_layer_norm_backward.restype = _i
+lib.infini_attn_layer_norm_backward_workspace_size.argtypes = [_ll, _i]
+lib.infini_attn_layer_norm_backward_workspace_size.restype = ctypes.c_size_t
+
+
 class InfiniAttnError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -162,6 +207,15 @@ def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Makes ``stream`` torch's current stream, so that the tensors a call returns belong to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _mode(mode: int, t: torch.Tensor) -> int:
@@ -378,6 +432,183 @@ def infini_attn_backward_workspace_size(B, H, L, N, dk, dv, mode=LINEAR, flags: 
     p.B, p.H, p.L, p.N, p.d_k, p.d_v, p.mode = int(B), int(H), int(L), int(N), int(dk), int(dv), int(mode)
     p.flags = int(flags)
     return int(lib.infini_attn_backward_workspace_size(ctypes.byref(p)))
+
+
+def _tensors(where: str, shapes: dict):
+    """Marshalling checks of the gated delta rule and the layer norm: name -> (tensor, shape, dtype); every tensor
+    with this shape and type, its last dimension contiguous, on one CUDA device.  Returns that device."""
+    dev = None
+    for name, (t, shape, dtype) in shapes.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a torch.Tensor")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    for name, (t, _, _) in shapes.items():
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be on a CUDA device, got {t.device}")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, the tensors before it on {dev}")
+        dev = t.device
+    return dev
+
+
+def _contiguous(where: str, **tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _rows_contiguous(where: str, **tensors):
+    for name, t in tensors.items():
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
+
+
+def _elem(where: str, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{where}: expected a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{where}: element type must be bfloat16 or float32, got {t.dtype}")
+    return t.dtype
+
+
+def _workspace(where: str, p, workspace):
+    if workspace is not None:
+        if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError(f"{where}: workspace must be a contiguous device tensor")
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.numel() * workspace.element_size()
+
+
+def _gated_delta_shapes(where, q, k, v, g, beta, lens):
+    """(B, H, Hk, L, dk, dv, the checks' table) of a gated delta sequence."""
+    t = _elem(where, q)
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError(f"{where}: q and v must have 4 dimensions")
+    B, Hk, L, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    f32 = torch.float32
+    table = dict(q=(q, (B, Hk, L, dk), t), k=(k, (B, Hk, L, dk), t), v=(v, (B, H, L, dv), t), g=(g, (B, H, L), f32),
+                 beta=(beta, (B, H, L), f32))
+    if lens is not None:
+        table["lens"] = (lens, (B,), torch.int32)
+    return B, H, Hk, L, dk, dv, table
+
+
+def infini_attn_gated_delta_forward(q, k, v, g, beta, S, out, scale: float = 0.0, lens=None, workspace=None,
+                                    stream=None, raise_on_error=True):
+    """Gated delta rule over whole sequences: S_t = e^g (S - beta k (k^T S)) + beta k v^T, out = scale S^T q.
+
+    q, k [B,Hk,L,dk], v, out [B,H,L,dv] (bf16 or fp32, any (B, head, L) strides); g (log decay), beta [B,H,L] fp32;
+    S [B,H,dk,dv] fp32, updated in place; lens: optional int32 [B] of row lengths on the device."""
+    where = "infini_attn_gated_delta_forward"
+    B, H, Hk, L, dk, dv, table = _gated_delta_shapes(where, q, k, v, g, beta, lens)
+    table["S"] = (S, (B, H, dk, dv), torch.float32)
+    table["out"] = (out, (B, H, L, dv), q.dtype)
+    dev = _tensors(where, table)
+    _contiguous(where, S=S, lens=lens)
+    _rows_contiguous(where, q=q, k=k, v=v, out=out)
+    p = GatedDeltaParams()
+    p.q, p.k, p.v, p.g, p.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
+    p.S, p.out, p.lens = S.data_ptr(), out.data_ptr(), _ptr(lens)
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv = B, H, Hk, L, dk, dv
+    p.mode, p.scale = _mode(0, q), float(scale)
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", out), ("g", g), ("beta", beta)):
+        getattr(p, f"{name}_stride")[:] = t.stride()[:3]
+    _workspace(where, p, workspace)
+    with torch.cuda.device(dev):
+        p.stream = _stream(stream)
+        rc = lib.infini_attn_gated_delta_forward(ctypes.byref(p))
+    return _check(rc, where, raise_on_error)
+
+
+def infini_attn_gated_delta_workspace_size(B, H, Hk, L, dk, dv, mode: int = 0) -> int:
+    p = GatedDeltaParams()
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv, p.mode = int(B), int(H), int(Hk), int(L), int(dk), int(dv), int(mode)
+    return int(lib.infini_attn_gated_delta_workspace_size(ctypes.byref(p)))
+
+
+def infini_attn_gated_delta_step(q_t, k_t, v_t, g, beta, S, out, slots=None, scale: float = 0.0, stream=None,
+                                 raise_on_error=True):
+    """One token of every request: q_t, k_t [B,Hk,dk], v_t, out [B,H,dv] (bf16 or fp32, any (B, head) strides),
+    g, beta [B,H] fp32; S [pool,H,dk,dv] fp32, updated in place.  slots: optional int32 [B], the state row of each
+    request (outside [0, pool): a padded request, nothing of it is read or written)."""
+    where = "infini_attn_gated_delta_step"
+    t = _elem(where, q_t)
+    if q_t.dim() != 3 or not isinstance(v_t, torch.Tensor) or v_t.dim() != 3 or not isinstance(S, torch.Tensor) \
+            or S.dim() != 4:
+        raise ValueError(f"{where}: q_t and v_t must have 3 dimensions and S 4")
+    B, Hk, dk = q_t.shape
+    H, dv = v_t.shape[1], v_t.shape[2]
+    f32 = torch.float32
+    table = dict(q_t=(q_t, (B, Hk, dk), t), k_t=(k_t, (B, Hk, dk), t), v_t=(v_t, (B, H, dv), t), g=(g, (B, H), f32),
+                 beta=(beta, (B, H), f32), S=(S, (S.shape[0], H, dk, dv), f32), out=(out, (B, H, dv), t))
+    if slots is not None:
+        table["slots"] = (slots, (B,), torch.int32)
+    dev = _tensors(where, table)
+    _contiguous(where, S=S, slots=slots)
+    _rows_contiguous(where, q_t=q_t, k_t=k_t, v_t=v_t, out=out)
+    p = GatedDeltaStepParams()
+    p.q, p.k, p.v, p.g, p.beta = q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), g.data_ptr(), beta.data_ptr()
+    p.S, p.out, p.slots = S.data_ptr(), out.data_ptr(), _ptr(slots)
+    p.B, p.H, p.Hk, p.pool, p.dk, p.dv = B, H, Hk, S.shape[0], dk, dv
+    p.mode, p.scale = _mode(0, q_t), float(scale)
+    for name, x in (("q", q_t), ("k", k_t), ("v", v_t), ("o", out), ("g", g), ("beta", beta)):
+        getattr(p, f"{name}_stride")[:] = x.stride()[:2]
+    with torch.cuda.device(dev):
+        p.stream = _stream(stream)
+        rc = lib.infini_attn_gated_delta_step(ctypes.byref(p))
+    return _check(rc, where, raise_on_error)
+
+
+def _layer_norm_args(where, x, weight, more):
+    t = _elem(where, x)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"{where}: x must have a last dimension to normalise")
+    D = x.shape[-1]
+    wt = _elem(where, weight)
+    table = dict(x=(x, x.shape, t), weight=(weight, (D,), wt))
+    for name, v in more.items():
+        if v is not None:
+            table[name] = (v, (D,), wt) if name == "bias" else (v, x.shape, t)
+    dev = _tensors(where, table)
+    _contiguous(where, x=x, weight=weight, **more)
+    return D, x.numel() // D, _mode(0, x) | (WEIGHT_F32 if wt == torch.float32 else 0), dev
+
+
+def infini_attn_layer_norm_forward(x, weight, bias, y, eps: float = 1e-5, stream=None, raise_on_error=True):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last dimension: x, y [..., D] contiguous, bf16 or
+    fp32 (y may be x); weight, bias [D] bf16 or fp32, bias may be None."""
+    where = "infini_attn_layer_norm_forward"
+    D, rows, mode, dev = _layer_norm_args(where, x, weight, dict(bias=bias, y=y))
+    with torch.cuda.device(dev):
+        rc = lib.infini_attn_layer_norm_forward(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), rows, D,
+                                                float(eps), mode, _stream(stream))
+    return _check(rc, where, raise_on_error)
+
+
+def infini_attn_layer_norm_backward(x, weight, d_y, eps: float = 1e-5, want_bias: bool = True, workspace=None,
+                                    stream=None, raise_on_error=True):
+    """Gradients of infini_attn_layer_norm_forward: returns (dx, dweight, dbias) as new device tensors (dbias is
+    None unless ``want_bias``); x, d_y [..., D] contiguous, one type; dweight, dbias in weight's type."""
+    where = "infini_attn_layer_norm_backward"
+    D, rows, mode, dev = _layer_norm_args(where, x, weight, dict(d_y=d_y))
+    p = GatedDeltaParams()
+    _workspace(where, p, workspace)
+    with torch.cuda.device(dev), _on(stream):
+        dx, dw = torch.empty_like(x), torch.empty_like(weight)
+        db = torch.empty_like(weight) if want_bias else None
+        rc = lib.infini_attn_layer_norm_backward(x.data_ptr(), weight.data_ptr(), d_y.data_ptr(), dx.data_ptr(),
+                                                 dw.data_ptr(), _ptr(db), rows, D, float(eps), mode, p.workspace,
+                                                 p.workspace_bytes, _stream(stream))
+    _check(rc, where, raise_on_error)
+    return dx, dw, db
+
+
+def infini_attn_layer_norm_backward_workspace_size(rows: int, D: int) -> int:
+    return int(lib.infini_attn_layer_norm_backward_workspace_size(int(rows), int(D)))
 
 
 def infini_attn_workspace_size(B, H, L, N, dk, dv, mode=LINEAR) -> int:

@@ -11,6 +11,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,7 +30,7 @@ def nvcc_path() -> str:
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
 
 
 def up_to_date() -> bool:
@@ -39,16 +41,7 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(LIBDIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc_path(), ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),
-           "-o", tmp, os.path.join(CSRC, "infini_attn.cu")]
-    extra = os.environ.get("INFINI_NVCC_FLAGS", "").split()
-    cmd[1:1] = extra + ["-Xptxas=-v"]
+def _run(cmd, verbose: bool) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -57,7 +50,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"nvcc failed with exit code {res.returncode}")
     if verbose:
         print(res.stdout + res.stderr, flush=True)
-    check_register_split(res.stdout + res.stderr)
+    return res.stdout + res.stderr
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = LIB + ".tmp"
+    extra = os.environ.get("INFINI_NVCC_FLAGS", "").split()
+    flags = [*extra, "-Xptxas=-v", ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
+             "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
+    with tempfile.TemporaryDirectory(dir=LIBDIR) as work:
+        units = [f for f in sources() if f.endswith(".cu")]
+        objs = [os.path.join(work, os.path.basename(u) + ".o") for u in units]
+        with ThreadPoolExecutor(len(units)) as pool:  # one nvcc per translation unit
+            logs = list(pool.map(lambda uo: _run([nvcc_path(), *flags, "-c", "-o", uo[1], uo[0]], verbose),
+                                 zip(units, objs)))
+        _run([nvcc_path(), ARCH, "-shared", "-o", tmp, *objs], verbose)
+    check_register_split("\n".join(logs))
     os.replace(tmp, LIB)
     return LIB
 

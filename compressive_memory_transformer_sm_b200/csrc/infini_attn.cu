@@ -28,6 +28,7 @@
 
 #include "../../include/infini_attn.h"
 #include "common.cuh"
+#include "host.h"
 #include "simt.cuh"
 #include "bwd_simt.cuh"
 #include "bwd_mem.cuh"
@@ -44,18 +45,12 @@ namespace infini {
 namespace {
 
 constexpr int kChunk = 128;        // tokens per update chunk
-constexpr int kSms = 148;          // B200 SM count: grid sizing (device independent, so plans are too)
 constexpr int kTargetCtas = 4 * kSms;  // CUDA-core update grid size aim
-constexpr size_t kAlign = 256;
 // Internal flag of forward_impl (not in the header): run the memory update
 // only -- no attention launch, no output -- for the decode step's fold.
 constexpr int kFlagUpdateOnly = 0x1000;
 
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
 // ------------------------------------------------------------ launch accounting
-enum Phase { kPhaseUpdate = 0, kPhaseState = 1, kPhaseAttn = 2, kPhasePre = 3, kPhaseProj = 4, kPhaseBwd = 5, kPhaseBwdTc = 6,
-             kPhaseBwdMemTc = 7, kPhases = 8 };
 std::atomic<long long> g_launches{0};
 std::atomic<int> g_profile_mask{0};
 struct EventPair {
@@ -69,7 +64,6 @@ std::vector<EventPair> g_prof;
 // it was created in): creating two events per timed launch would add host time
 // to every timed call.
 std::vector<std::pair<unsigned long long, cudaEvent_t>> g_event_pool;
-unsigned long long current_context_id();
 
 cudaEvent_t take_timing_event(unsigned long long ctx) {
   {
@@ -90,36 +84,31 @@ cudaEvent_t take_timing_event(unsigned long long ctx) {
   return e;
 }
 
-// Counts one kernel launch and, when its phase is being timed, brackets it
-// with events on `stream`.  Construct right before the launch, destroy
-// right after it.
-struct LaunchScope {
-  int phase;
-  cudaStream_t stream;
-  cudaEvent_t a = nullptr, b = nullptr;
-  unsigned long long ctx = 0;
-  LaunchScope(int ph, cudaStream_t st) : phase(ph), stream(st) {
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    if (g_profile_mask.load(std::memory_order_relaxed) & (1 << ph)) {
-      ctx = current_context_id();
-      a = take_timing_event(ctx);
-      b = a ? take_timing_event(ctx) : nullptr;
-      if (a && b) {
-        cudaEventRecord(a, stream);
-      } else {
-        if (a) cudaEventDestroy(a);
-        a = b = nullptr;
-      }
-    }
-  }
-  ~LaunchScope() {
+}  // namespace
+
+LaunchScope::LaunchScope(int ph, cudaStream_t st) : phase(ph), stream(st) {
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (g_profile_mask.load(std::memory_order_relaxed) & (1 << ph)) {
+    ctx = current_context_id();
+    a = take_timing_event(ctx);
+    b = a ? take_timing_event(ctx) : nullptr;
     if (a && b) {
-      cudaEventRecord(b, stream);
-      std::lock_guard<std::mutex> lk(g_prof_mu);
-      g_prof.push_back({phase, a, b, ctx});
+      cudaEventRecord(a, stream);
+    } else {
+      if (a) cudaEventDestroy(a);
+      a = b = nullptr;
     }
   }
-};
+}
+LaunchScope::~LaunchScope() {
+  if (a && b) {
+    cudaEventRecord(b, stream);
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    g_prof.push_back({phase, a, b, ctx});
+  }
+}
+
+namespace {
 
 struct Plan {
   int B, H, N, dk, dv, mode, S, G, cpb, nseg_part;
@@ -196,6 +185,8 @@ EncodeTiledFn get_encode() {
   return fn;
 }
 
+}  // namespace
+
 // Unique id of the CUDA context current on this thread (0 if none or on
 // failure).  Per-context caches key on it rather than on the device ordinal:
 // a context that is destroyed and recreated (cudaDeviceReset, a primary
@@ -222,6 +213,8 @@ unsigned long long current_context_id() {
     return 0;
   return id;
 }
+
+namespace {
 
 // 4-D map over a [B, H, L, 128] bf16 tensor with element strides st[0..2]
 // (d contiguous); box 64 x 128 tokens, 128-byte swizzle.
@@ -250,14 +243,21 @@ bool encode_rows(CUtensorMap* m, const void* ptr, long long rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn) {
   const char* x = static_cast<const char*>(a);
   const char* y = static_cast<const char*>(b);
   return x < y + bn && y < x + an;
 }
+
+namespace {
+
 size_t extent_bytes(const long long st[3], int B, int H, long long L, int d, size_t es) {
   return (size_t)(((long long)(B - 1) * st[0] + (long long)(H - 1) * st[1] + (L - 1) * st[2] + d) * (long long)es);
 }
+
+}  // namespace
 
 int check_device(bool need_tc) {
   (void)need_tc;
@@ -273,6 +273,8 @@ int check_device(bool need_tc) {
   ok_ctx = ctx;
   return INFINI_OK;
 }
+
+namespace {
 
 // The fork and join events of one-segment calls, created once per thread and
 // context (a pair shared between threads could interleave their records).
@@ -303,8 +305,10 @@ bool fork_events(cudaEvent_t* ev_fork, cudaEvent_t* ev_join) {
   return true;
 }
 
+}  // namespace
+
 // The CUDA error behind the most recent INFINI_ERR_LAUNCH (any thread).
-std::atomic<int> g_last_cuda_error{0};
+static std::atomic<int> g_last_cuda_error{0};
 int note_cuda_error(cudaError_t e) {
   g_last_cuda_error.store((int)e);
   return INFINI_ERR_LAUNCH;
@@ -313,6 +317,8 @@ int launch_status() {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? INFINI_OK : note_cuda_error(e);
 }
+
+namespace {
 
 // What the local attention (Eq. 6) reads: q, k themselves, or their rotated
 // copies in the workspace when position embeddings are on (then qm is the
@@ -492,6 +498,8 @@ cudaMemPool_t workspace_pool() {
   return pool;
 }
 
+}  // namespace
+
 // Stream-ordered workspace allocation (released with cudaFreeAsync).
 bool ws_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
   cudaMemPool_t pool = workspace_pool();
@@ -503,6 +511,8 @@ bool ws_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
   }
   return true;
 }
+
+namespace {
 
 // The dynamic shared-memory limit is an attribute of a function in the
 // current context: set it for the tensor-core kernels once for every context

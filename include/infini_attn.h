@@ -72,6 +72,8 @@ extern "C" {
 #define INFINI_DELTA 0x1  /* Eq. 9 */
 /* element type of q, k, v and out: bf16 unless this bit is set */
 #define INFINI_F32 0x10
+/* layer norm only: weight, bias and their gradients are fp32, not bf16 */
+#define INFINI_WEIGHT_F32 0x20
 /* infini_attn_params.flags: run the CUDA-core (SIMT) kernels even where the
  * tensor-core kernels apply -- a second GPU implementation, for testing */
 #define INFINI_FLAG_FORCE_SIMT 0x1
@@ -323,6 +325,109 @@ INFINI_API int infini_attn_backward(const infini_attn_bwd_params* p);
 INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_params* p);
 
 /*
+ * Gated delta rule: the delta rule's memory with a decay and a write strength
+ * per token, without a feature map and without a segment's local attention
+ * ("Gated Delta Networks: Improving Mamba2 with Delta Rule", arXiv 2412.06464,
+ * its Eq. 10).  Per (batch row b, value head h), with a state S [dk, dv]:
+ *   S'  = exp(g_t) S_{t-1}
+ *   u_t = beta_t (v_t - S'^T k_t)
+ *   S_t = S' + k_t u_t^T
+ *   o_t = scale S_t^T q_t
+ * H value heads share Hk key heads (H a multiple of Hk): value head h reads
+ * q, k of key head h / (H / Hk).  q, k [B, Hk, L, dk], v, out [B, H, L, dv],
+ * bf16 or (mode INFINI_F32) fp32, any strides of (B, head, L) with the last
+ * dimension contiguous; all zero selects the contiguous layout.  g, beta
+ * [B, H, L] fp32 with strides of their own; S [B, H, dk, dv] fp32,
+ * contiguous.  1 <= dk, dv <= 128.
+ *
+ * g is the logarithm of the decay, g <= 0 in use; -inf (or anything whose
+ * exponential is 0) clears the state before the token.  Keys are used as they
+ * are given: the recurrence contracts while beta |k|^2 <= 2, which keys of
+ * unit length and beta in [0, 2] meet.
+ *
+ * lens (optional, device, int32 [B]): row b has lens[b] tokens, values below 0
+ * and above L count as 0 and L.  Tokens at and past lens[b] are padding and
+ * are not read: their rows of `out` are left as they were, the state is the
+ * one after token lens[b] - 1, and their gradients are written as 0.
+ *
+ * All products and sums are fp32 or better, and so is the state; out, dq, dk
+ * and dv are rounded once, to their type.  Results do not depend on the other
+ * batch rows and heads, and repeat bit for bit.
+ */
+typedef struct infini_attn_gated_delta_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  float* S;  /* on entry S_0, on return the state after the last token */
+  void* out;
+  const int* lens; /* NULL: every row has L tokens */
+  int B, H, Hk;
+  long long L;
+  int dk, dv;
+  int mode;    /* 0 or INFINI_F32 */
+  float scale; /* 0 selects 1/sqrt(dk) */
+  long long q_stride[3], k_stride[3], v_stride[3], o_stride[3], g_stride[3], beta_stride[3];
+  /* caller workspace (256-byte aligned); NULL lets the call take its own on `stream` */
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} infini_attn_gated_delta_params;
+
+/* Whole sequences: out, and S updated in place.  `out` must not overlap the inputs. */
+INFINI_API int infini_attn_gated_delta_forward(const infini_attn_gated_delta_params* p);
+
+/* Bytes of workspace the forward needs (0 if the shape is invalid; may be 0 for short sequences). */
+INFINI_API size_t infini_attn_gated_delta_workspace_size(const infini_attn_gated_delta_params* p);
+
+/*
+ * One token of B requests (serving): q_t, k_t [B, Hk, dk], v_t, out [B, H, dv], g, beta [B, H]; strides of
+ * (B, head), all zero selects the contiguous layout.  S [pool, H, dk, dv] fp32 is a pool of states: request b
+ * owns row slots[b] (device, int32; NULL: row b, and pool >= B), updated in place.  A slot outside [0, pool) is a
+ * padded request: nothing of it is read or written.  Requests that name the same slot advance it one after the
+ * other, in the order of b.  No workspace, no allocation.
+ */
+typedef struct infini_attn_gated_delta_step_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  float* S;
+  void* out;
+  const int* slots;
+  int B, H, Hk;
+  long long pool;
+  int dk, dv;
+  int mode;
+  float scale;
+  long long q_stride[2], k_stride[2], v_stride[2], o_stride[2], g_stride[2], beta_stride[2];
+  cudaStream_t stream;
+} infini_attn_gated_delta_step_params;
+
+INFINI_API int infini_attn_gated_delta_step(const infini_attn_gated_delta_step_params* p);
+
+/*
+ * Layer normalisation of `rows` contiguous rows of D elements (1 <= D <= 16384):
+ * y = (x - mean) / sqrt(var + eps) * weight + bias.  x, y bf16 or (mode
+ * INFINI_F32) fp32; weight, bias [D] bf16 or (INFINI_WEIGHT_F32) fp32; bias may
+ * be NULL; y may be x.  fp32 arithmetic; y is rounded once.
+ */
+INFINI_API int infini_attn_layer_norm_forward(const void* x, const void* weight, const void* bias, void* y,
+                                              long long rows, int D, float eps, int mode, cudaStream_t stream);
+
+/*
+ * Its gradients from dy: dx (x's type; may be dy or x), dweight and, unless NULL, dbias (weight's type, summed over
+ * the rows in fp32 in a fixed order).  The statistics are taken from x again.  Workspace as elsewhere:
+ * infini_attn_layer_norm_backward_workspace_size(rows, D) bytes, 256-byte aligned, or NULL.
+ */
+INFINI_API int infini_attn_layer_norm_backward(const void* x, const void* weight, const void* dy, void* dx,
+                                               void* dweight, void* dbias, long long rows, int D, float eps, int mode,
+                                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+INFINI_API size_t infini_attn_layer_norm_backward_workspace_size(long long rows, int D);
+
+/*
  * Workspace that the library allocates itself (calls given no workspace)
  * comes from a stream-ordered pool of its own, one per CUDA context, that
  * keeps freed blocks for the next call.  This returns the pool's unused
@@ -381,6 +486,8 @@ INFINI_API int infini_attn_last_cuda_error(char* name, int n);
 
 /* sizeof(infini_attn_params), for bindings that build the struct themselves. */
 INFINI_API size_t infini_attn_params_size(void);
+/* The same of infini_attn_gated_delta_params (0), its step's (1) and its backward's (2) struct; 0 otherwise. */
+INFINI_API size_t infini_attn_gated_delta_params_size(int which);
 
 /* Which kernels the given arguments would run: 1 tensor-core, 0 CUDA-core, <0 error code. */
 INFINI_API int infini_attn_path(int dk, int dv, int mode, int flags);

@@ -1,0 +1,128 @@
+"""Refusals of the gated delta rule's and the layer norm's calls, and their structs' layouts (no kernel is launched)."""
+
+import ctypes
+
+import pytest
+import torch
+
+from compressive_memory_transformer_sm_b200 import F32, api
+
+OK = (api.INFINI_OK, api.INFINI_ERR_DEVICE)  # a well-formed call: OK is not reached without a device
+
+
+def host(n=1 << 16):
+    return ctypes.addressof(_BUF) + 256 - ctypes.addressof(_BUF) % 256 + n
+
+
+_BUF = ctypes.create_string_buffer(1 << 22)
+
+
+def params(**over):
+    p = api.GatedDeltaParams()
+    p.q, p.k, p.v, p.g, p.beta, p.S, p.out = (host(i << 18) for i in range(1, 8))
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv, p.mode = 1, 2, 1, 4, 16, 8, F32
+    for n, x in over.items():
+        setattr(p, n, x)
+    return p
+
+
+def step_params(**over):
+    p = api.GatedDeltaStepParams()
+    p.q, p.k, p.v, p.g, p.beta, p.S, p.out = (host(i << 18) for i in range(1, 8))
+    p.B, p.H, p.Hk, p.pool, p.dk, p.dv, p.mode = 2, 2, 1, 4, 16, 8, 0
+    for n, x in over.items():
+        setattr(p, n, x)
+    return p
+
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host pointers: refusals only, on machines without a GPU")
+
+
+def test_struct_sizes():
+    for which, cls in enumerate((api.GatedDeltaParams, api.GatedDeltaStepParams)):
+        assert api.lib.infini_attn_gated_delta_params_size(which) == ctypes.sizeof(cls)
+    assert api.lib.infini_attn_gated_delta_params_size(7) == 0
+
+
+def forward(**over):
+    return api.lib.infini_attn_gated_delta_forward(ctypes.byref(params(**over)))
+
+
+def step(**over):
+    return api.lib.infini_attn_gated_delta_step(ctypes.byref(step_params(**over)))
+
+
+BAD, UNSUP = api.INFINI_ERR_INVALID_ARG, api.INFINI_ERR_UNSUPPORTED
+L3, L2 = ctypes.c_longlong * 3, ctypes.c_longlong * 2
+
+
+def test_well_formed_calls_reach_the_device_check():
+    assert forward() == api.INFINI_ERR_DEVICE and step() == api.INFINI_ERR_DEVICE
+
+
+@pytest.mark.parametrize("over,rc", [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(g=None), BAD), (dict(beta=None), BAD),
+    (dict(S=None), BAD), (dict(out=None), BAD), (dict(B=0), BAD), (dict(H=3, Hk=2), BAD), (dict(L=0), BAD),
+    (dict(dk=0), BAD), (dict(dv=-1), BAD), (dict(dk=129), UNSUP), (dict(dv=200), UNSUP), (dict(mode=1), UNSUP),
+    (dict(L=1 << 32), UNSUP), (dict(q_stride=L3(-16, 0, 16)), BAD), (dict(o_stride=L3(64, 32, 4)), BAD),
+    (dict(o_stride=L3(0, 0, 8)), BAD), (dict(B=2, o_stride=L3(8, 0, 16)), BAD),
+])
+def test_forward_refusals(over, rc):
+    assert forward(**over) == rc
+
+
+def test_overlaps_are_refused():
+    p = params()
+    assert forward(out=p.v) == BAD and forward(S=p.k) == BAD and forward(out=p.S) == BAD and forward(lens=p.out) == BAD
+    s = step_params()
+    assert step(out=s.q) == BAD and step(S=s.v) == BAD and step(slots=s.S) == BAD
+
+
+@pytest.mark.parametrize("over,rc", [
+    (dict(S=None), BAD), (dict(B=0), BAD), (dict(H=3, Hk=2), BAD), (dict(pool=0), BAD), (dict(pool=1), BAD),
+    (dict(dk=144), UNSUP), (dict(mode=0x20), UNSUP), (dict(pool=1 << 60), UNSUP), (dict(o_stride=L2(8, 8)), BAD),
+    (dict(v_stride=L2(-1, 8)), BAD),
+])
+def test_step_refusals(over, rc):
+    assert step(**over) == rc
+
+
+def test_layer_norm_refusals():
+    f, b = api.lib.infini_attn_layer_norm_forward, api.lib.infini_attn_layer_norm_backward
+    x, w, y, z = (host(i << 18) for i in range(1, 5))
+    assert f(x, w, None, y, 4, 32, 1e-5, 0, None) == api.INFINI_ERR_DEVICE
+    assert f(x, w, None, x, 4, 32, 1e-5, 0, None) == api.INFINI_ERR_DEVICE
+    assert f(None, w, None, y, 4, 32, 1e-5, 0, None) == BAD and f(x, None, None, y, 4, 32, 1e-5, 0, None) == BAD
+    assert f(x, w, None, y, 0, 32, 1e-5, 0, None) == BAD and f(x, w, None, y, 4, 0, 1e-5, 0, None) == BAD
+    assert f(x, w, None, y, 4, 32, -1.0, 0, None) == BAD and f(x, w, None, y, 4, 32, float("nan"), 0, None) == BAD
+    assert f(x, w, None, x + 64, 4, 32, 1e-5, 0, None) == BAD and f(x, w, y, y, 4, 32, 1e-5, 0, None) == BAD
+    assert f(x, w, None, y, 4, 16385, 1e-5, 0, None) == UNSUP and f(x, w, None, y, 4, 32, 1e-5, 1, None) == UNSUP
+    n = api.infini_attn_layer_norm_backward_workspace_size(4, 32)
+    assert n > 0 and api.infini_attn_layer_norm_backward_workspace_size(4, 1 << 20) == 0
+    dw, db, ws = (host((8 + i) << 18) for i in range(3))
+    assert b(x, w, y, z, dw, db, 4, 32, 1e-5, 0, ws, n, None) == api.INFINI_ERR_DEVICE
+    assert b(x, w, y, y, dw, None, 4, 32, 1e-5, 0, ws, n, None) == api.INFINI_ERR_DEVICE
+    assert b(x, w, y, z, dw, dw, 4, 32, 1e-5, 0, ws, n, None) == BAD
+    assert b(x, w, y, z, w, db, 4, 32, 1e-5, 0, ws, n, None) == BAD
+    assert b(x, w, y, z, dw, db, 4, 32, 1e-5, 0, ws, n - 1, None) == api.INFINI_ERR_WORKSPACE
+    assert b(x, w, y, z, dw, db, 4, 32, 1e-5, 0, ws + 16, n, None) == api.INFINI_ERR_WORKSPACE
+
+
+def test_binding_refuses_what_it_cannot_pass_on():
+    z = torch.zeros
+    q, k, v = z(1, 2, 4, 16), z(1, 2, 4, 16), z(1, 2, 4, 8)
+    g, S = z(1, 2, 4), z(1, 2, 16, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.infini_attn_gated_delta_forward(q, k, v, g, g, S, z(1, 2, 4, 8))
+    with pytest.raises(ValueError, match="shape"):
+        api.infini_attn_gated_delta_forward(q, k, v, g, g[:, :1], S, z(1, 2, 4, 8))
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        api.infini_attn_gated_delta_forward(q.half(), k, v, g, g, S, v)
+    with pytest.raises(TypeError):
+        api.infini_attn_gated_delta_forward(q, None, v, g, g, S, v)
+    with pytest.raises(ValueError, match="dimensions"):
+        api.infini_attn_gated_delta_step(q, k, v, g, g, S, v)
+    with pytest.raises(ValueError, match="shape"):
+        api.infini_attn_layer_norm_forward(z(3, 4), z(5), None, z(3, 4))
+    with pytest.raises(ValueError, match="must be"):
+        api.infini_attn_layer_norm_forward(z(3, 4), z(4), None, z(3, 4, dtype=torch.bfloat16))
