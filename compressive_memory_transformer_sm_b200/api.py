@@ -43,7 +43,8 @@ EXPORTED = (
     "infini_attn_backward_workspace_size", "infini_attn_trim_workspace", "infini_attn_last_cuda_error",
     "infini_attn_gated_delta_forward", "infini_attn_gated_delta_workspace_size", "infini_attn_gated_delta_step",
     "infini_attn_gated_delta_params_size", "infini_attn_layer_norm_forward", "infini_attn_layer_norm_backward",
-    "infini_attn_layer_norm_backward_workspace_size",
+    "infini_attn_layer_norm_backward_workspace_size", "infini_attn_gated_delta_backward",
+    "infini_attn_gated_delta_backward_workspace_size",
 )
 WEIGHT_F32 = 0x20
 
@@ -159,6 +160,23 @@ class GatedDeltaStepParams(ctypes.Structure):
     ]
 
 
+class GatedDeltaBackwardParams(ctypes.Structure):
+    """Mirror of ``infini_attn_gated_delta_backward_params`` (include/infini_attn.h)."""
+
+    _fields_ = [
+        ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp), ("beta", _vp), ("S0", _vp), ("d_out", _vp), ("dS_L", _vp),
+        ("lens", _vp), ("dq", _vp), ("dk_out", _vp), ("dv_out", _vp), ("dg", _vp), ("dbeta", _vp), ("dS0", _vp),
+        ("B", _i), ("H", _i), ("Hk", _i), ("L", _ll), ("dk", _i), ("dv", _i), ("mode", _i), ("scale", ctypes.c_float),
+        ("q_stride", _ll * 3), ("k_stride", _ll * 3), ("v_stride", _ll * 3), ("d_out_stride", _ll * 3),
+        ("g_stride", _ll * 3), ("beta_stride", _ll * 3),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+lib.infini_attn_gated_delta_backward.argtypes = [ctypes.POINTER(GatedDeltaBackwardParams)]
+lib.infini_attn_gated_delta_backward.restype = _i
+lib.infini_attn_gated_delta_backward_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaBackwardParams)]
+lib.infini_attn_gated_delta_backward_workspace_size.restype = ctypes.c_size_t
 lib.infini_attn_gated_delta_forward.argtypes = [ctypes.POINTER(GatedDeltaParams)]
 lib.infini_attn_gated_delta_forward.restype = _i
 lib.infini_attn_gated_delta_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaParams)]
@@ -528,6 +546,48 @@ def infini_attn_gated_delta_workspace_size(B, H, Hk, L, dk, dv, mode: int = 0) -
     p = GatedDeltaParams()
     p.B, p.H, p.Hk, p.L, p.dk, p.dv, p.mode = int(B), int(H), int(Hk), int(L), int(dk), int(dv), int(mode)
     return int(lib.infini_attn_gated_delta_workspace_size(ctypes.byref(p)))
+
+
+def infini_attn_gated_delta_backward(q, k, v, g, beta, d_out, S0=None, dS_L=None, scale: float = 0.0, lens=None,
+                                     want_state_grad: bool = True, workspace=None, stream=None, raise_on_error=True):
+    """Gradients of infini_attn_gated_delta_forward started from S0 (None: zero), from d_out and dS_L (None: zero).
+
+    Returns (dq, dk, dv, dg, dbeta, dS0) as new contiguous device tensors, dq, dk, dv in the inputs' type and the
+    others fp32; dS0 is None unless ``want_state_grad``.  Layouts as for the forward, d_out like out."""
+    where = "infini_attn_gated_delta_backward"
+    B, H, Hk, L, dk, dv, table = _gated_delta_shapes(where, q, k, v, g, beta, lens)
+    table["d_out"] = (d_out, (B, H, L, dv), q.dtype)
+    for name, t in (("S0", S0), ("dS_L", dS_L)):
+        if t is not None:
+            table[name] = (t, (B, H, dk, dv), torch.float32)
+    dev = _tensors(where, table)
+    _contiguous(where, S0=S0, dS_L=dS_L, lens=lens)
+    _rows_contiguous(where, q=q, k=k, v=v, d_out=d_out)
+    p = GatedDeltaBackwardParams()
+    p.q, p.k, p.v, p.g, p.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
+    p.S0, p.d_out, p.dS_L, p.lens = _ptr(S0), d_out.data_ptr(), _ptr(dS_L), _ptr(lens)
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv = B, H, Hk, L, dk, dv
+    p.mode, p.scale = _mode(0, q), float(scale)
+    for name, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out), ("g", g), ("beta", beta)):
+        getattr(p, f"{name}_stride")[:] = t.stride()[:3]
+    _workspace(where, p, workspace)
+    with torch.cuda.device(dev), _on(stream):
+        new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        dq, dkk, dvv = new(B, Hk, L, dk, dtype=q.dtype), new(B, Hk, L, dk, dtype=q.dtype), new(B, H, L, dv, dtype=q.dtype)
+        dg, dbeta = new(B, H, L), new(B, H, L)
+        dS0 = new(B, H, dk, dv) if want_state_grad else None
+        p.dq, p.dk_out, p.dv_out = dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr()
+        p.dg, p.dbeta, p.dS0 = dg.data_ptr(), dbeta.data_ptr(), _ptr(dS0)
+        p.stream = _stream(stream)
+        rc = lib.infini_attn_gated_delta_backward(ctypes.byref(p))
+    _check(rc, where, raise_on_error)
+    return dq, dkk, dvv, dg, dbeta, dS0
+
+
+def infini_attn_gated_delta_backward_workspace_size(B, H, Hk, L, dk, dv, mode: int = 0) -> int:
+    p = GatedDeltaBackwardParams()
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv, p.mode = int(B), int(H), int(Hk), int(L), int(dk), int(dv), int(mode)
+    return int(lib.infini_attn_gated_delta_backward_workspace_size(ctypes.byref(p)))
 
 
 def infini_attn_gated_delta_step(q_t, k_t, v_t, g, beta, S, out, slots=None, scale: float = 0.0, stream=None,

@@ -1,4 +1,4 @@
-// Host side of the gated delta rule: infini_attn_gated_delta_forward, _step.
+// Host side of the gated delta rule: infini_attn_gated_delta_forward, _step, _backward.
 #include <math.h>
 #include <string.h>
 
@@ -7,6 +7,7 @@
 #include "../../include/infini_attn.h"
 #include "common.cuh"
 #include "gated_delta.cuh"
+#include "gd_chunk.cuh"
 #include "host.h"
 
 namespace infini {
@@ -58,6 +59,10 @@ int check_shape(const Shape& s) {
   return INFINI_OK;
 }
 
+bool space_ok(const void* ws, size_t bytes, size_t need) {
+  return !ws || (bytes >= need && reinterpret_cast<uintptr_t>(ws) % kAlign == 0);
+}
+
 int launch_recur(const RecurArgs& a, bool f32, cudaStream_t st) {
   const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.S) % 16 == 0;
   const dim3 grid((a.dv + kRecurCols - 1) / kRecurCols, a.H, a.B);
@@ -69,6 +74,110 @@ int launch_recur(const RecurArgs& a, bool f32, cudaStream_t st) {
         : recur_kernel<__nv_bfloat16, false><<<grid, kRecurThreads, 0, st>>>(a);
   return launch_status();
 }
+
+// Whether rows of d elements can be read and written 16 bytes at a time.
+bool rows_vec(const void* p, const long long st[3], int d, size_t es) {
+  const long long v = 16 / (long long)es;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && d % v == 0 && st[0] % v == 0 && st[1] % v == 0 && st[2] % v == 0;
+}
+
+// ---------------------------------------------------------------- chunked
+int padded_dk(int dk) { return dk <= 64 ? 64 : 128; }
+int col_warps(int dv) { return (dv + 15) / 16; }
+
+// Workspace of nc chunks of every (b, h).
+struct ChunkSpace {
+  size_t T, P, vec, G, snap, dsnap, acc, bytes;
+  ChunkSpace(const Shape& s, long long nc, bool bwd) {
+    const size_t n = (size_t)s.B * s.H * nc, state = (size_t)col_warps(s.dv) * padded_dk(s.dk) * 16 * 4;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+      const size_t was = at;
+      at += align_up(bytes);
+      return was;
+    };
+    T = take(n * kTri * 4);
+    P = take(n * kTri * 4);
+    vec = take(n * kVec * 4);
+    G = take(n * kC * 8);
+    snap = take(bwd ? n * state : 0);
+    dsnap = take(bwd ? n * state : 0);
+    acc = take(bwd && s.H > s.Hk ? (size_t)s.B * s.Hk * nc * 2 * kC * padded_dk(s.dk) * 4 : 0);
+    bytes = at;
+  }
+  void place(ChunkArgs& a, void* ws) const {
+    char* w = static_cast<char*>(ws);
+    a.T = reinterpret_cast<float*>(w + T);
+    a.P = reinterpret_cast<float*>(w + P);
+    a.vec = reinterpret_cast<float*>(w + vec);
+    a.G = reinterpret_cast<double*>(w + G);
+    a.snap = reinterpret_cast<float4*>(w + snap);
+    a.dsnap = reinterpret_cast<float4*>(w + dsnap);
+    a.acc = reinterpret_cast<float*>(w + acc);
+  }
+};
+
+// The forward works through a long sequence in slabs of chunks, so that its workspace stays below this.
+constexpr size_t kSlabBytes = size_t(1) << 30;
+long long all_chunks(const Shape& s) { return (s.L + kC - 1) / kC; }
+long long slab_chunks(const Shape& s) {
+  const size_t one = (size_t)s.B * s.H * (2 * kTri * 4 + kVec * 4 + kC * 8);
+  return std::max<long long>(1, std::min<long long>(all_chunks(s), (long long)(kSlabBytes / one)));
+}
+
+// The dynamic shared-memory limit is an attribute of a function in the current context.
+template <typename F> int allow_smem(F* kernel, size_t bytes) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return e == cudaSuccess ? INFINI_OK : note_cuda_error(e);
+}
+template <typename F> int launch_chunk(F* kernel, dim3 grid, int threads, size_t smem, int phase, const ChunkArgs& a, cudaStream_t st) {
+  const int rc = allow_smem(kernel, smem);
+  if (rc != INFINI_OK) return rc;
+  LaunchScope scope(phase, st);
+  kernel<<<grid, threads, smem, st>>>(a);
+  return launch_status();
+}
+
+// Warps of a state block: as few as keep the blocks within one per SM, so that few heads spread over many SMs.
+int warps_per_block(int nw, long long heads) {
+  int w = 1;
+  while (w < kMaxWarps && w < nw && heads * ((nw + w - 1) / w) > kSms) w *= 2;
+  return w;
+}
+
+template <typename T, int DK> int run_prep(const ChunkArgs& a, cudaStream_t st) {
+  return launch_chunk(prep_kernel<T, DK>, dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
+}
+template <typename T, int DK, bool OUT> int run_state(ChunkArgs a, cudaStream_t st) {
+  const int nw = col_warps(a.dv);
+  a.wpc = warps_per_block(nw, (long long)a.B * a.H);
+  return launch_chunk(state_kernel<T, DK, OUT>, dim3((nw + a.wpc - 1) / a.wpc, a.H, a.B), std::max(128, 32 * a.wpc),
+                      kStages<T> * sizeof(StateSmem<T, DK>), kPhaseState, a, st);
+}
+template <typename T, int DK> int chunk_forward(ChunkArgs a, long long chunks, long long slab, cudaStream_t st) {
+  for (long long c = 0; c < chunks; c += slab) {
+    a.c0 = (int)c;
+    a.nc = (int)std::min(slab, chunks - c);
+    int rc = run_prep<T, DK>(a, st);
+    if (rc == INFINI_OK) rc = run_state<T, DK, true>(a, st);
+    if (rc != INFINI_OK) return rc;
+  }
+  return INFINI_OK;
+}
+template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
+  int rc = run_prep<T, DK>(a, st);
+  if (rc == INFINI_OK) rc = run_state<T, DK, false>(a, st);
+  if (rc != INFINI_OK) return rc;
+  const int nw = col_warps(a.dv);
+  a.wpc = warps_per_block(nw, (long long)a.B * a.H);
+  rc = launch_chunk(bwd_state_kernel<T, DK>, dim3((nw + a.wpc - 1) / a.wpc, a.H, a.B), std::max(128, 32 * a.wpc),
+                    kStages<T> * sizeof(StateSmem<T, DK>), kPhaseBwd, a, st);
+  if (rc != INFINI_OK) return rc;
+  return launch_chunk(grad_kernel<T, DK>, dim3(a.nc, a.Hk, a.B), 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
+}
+
+// Sequences of fewer tokens than this go token by token.
+constexpr long long kChunkFrom = 32;
 
 int forward(infini_attn_gated_delta_params p) {
   if (!p.q || !p.k || !p.v || !p.g || !p.beta || !p.S || !p.out) return INFINI_ERR_INVALID_ARG;
@@ -98,8 +207,36 @@ int forward(infini_attn_gated_delta_params p) {
   for (const Range& x : ins)
     if (x.p && (ranges_overlap(out.p, out.n, x.p, x.n) || ranges_overlap(S.p, S.n, x.p, x.n))) return INFINI_ERR_INVALID_ARG;
   if (ranges_overlap(out.p, out.n, S.p, S.n)) return INFINI_ERR_INVALID_ARG;
+  if (!space_ok(p.workspace, p.workspace_bytes, infini_attn_gated_delta_workspace_size(&p))) return INFINI_ERR_WORKSPACE;
   rc = check_device(false);
   if (rc != INFINI_OK) return rc;
+  const Shape shape{p.B, p.H, p.Hk, p.dk, p.dv, p.mode, p.L};
+  const float scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)p.dk);
+  if (p.L >= kChunkFrom) {
+    const long long slab = slab_chunks(shape);
+    const ChunkSpace space(shape, slab, false);
+    void* w = p.workspace;
+    if (!w && !ws_alloc(&w, space.bytes, p.stream)) return INFINI_ERR_WORKSPACE;
+    ChunkArgs a = {};
+    a.q = p.q; a.k = p.k; a.v = p.v; a.g = p.g; a.beta = p.beta; a.lens = p.lens; a.S = p.S; a.out = p.out;
+    memcpy(a.qs, p.q_stride, sizeof(a.qs));
+    memcpy(a.ks, p.k_stride, sizeof(a.ks));
+    memcpy(a.vs, p.v_stride, sizeof(a.vs));
+    memcpy(a.os, p.o_stride, sizeof(a.os));
+    memcpy(a.gs, p.g_stride, sizeof(a.gs));
+    memcpy(a.bs, p.beta_stride, sizeof(a.bs));
+    a.L = p.L; a.B = p.B; a.H = p.H; a.Hk = p.Hk; a.group = p.H / p.Hk; a.dk = p.dk; a.dv = p.dv; a.scale = scale;
+    a.vec_k = rows_vec(p.q, p.q_stride, p.dk, es) && rows_vec(p.k, p.k_stride, p.dk, es);
+    a.vec_v = rows_vec(p.v, p.v_stride, p.dv, es);
+    a.vec_o = rows_vec(p.out, p.o_stride, p.dv, es);
+    space.place(a, w);
+    const bool wide = padded_dk(p.dk) == 128;
+    const long long n = all_chunks(shape);
+    rc = f32 ? wide ? chunk_forward<float, 128>(a, n, slab, p.stream) : chunk_forward<float, 64>(a, n, slab, p.stream)
+             : wide ? chunk_forward<bf16, 128>(a, n, slab, p.stream) : chunk_forward<bf16, 64>(a, n, slab, p.stream);
+    if (!p.workspace && cudaFreeAsync(w, p.stream) != cudaSuccess && rc == INFINI_OK) rc = INFINI_ERR_WORKSPACE;
+    return rc;
+  }
   RecurArgs a = {};
   a.q = p.q; a.k = p.k; a.v = p.v; a.g = p.g; a.beta = p.beta; a.S = p.S; a.out = p.out; a.lens = p.lens;
   memcpy(a.qs, p.q_stride, sizeof(a.qs));
@@ -109,8 +246,71 @@ int forward(infini_attn_gated_delta_params p) {
   memcpy(a.gs, p.g_stride, sizeof(a.gs));
   memcpy(a.bs, p.beta_stride, sizeof(a.bs));
   a.L = p.L; a.pool = p.B; a.B = p.B; a.H = p.H; a.group = p.H / p.Hk; a.dk = p.dk; a.dv = p.dv;
-  a.scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)p.dk);
+  a.scale = scale;
   return launch_recur(a, f32, p.stream);
+}
+
+int backward(infini_attn_gated_delta_backward_params p) {
+  if (!p.q || !p.k || !p.v || !p.g || !p.beta || !p.d_out || !p.dq || !p.dk_out || !p.dv_out || !p.dg || !p.dbeta)
+    return INFINI_ERR_INVALID_ARG;
+  const Shape shape{p.B, p.H, p.Hk, p.dk, p.dv, p.mode, p.L};
+  int rc = check_shape(shape);
+  if (rc != INFINI_OK) return rc;
+  fill_strides(p.q_stride, p.Hk, p.L, p.dk);
+  fill_strides(p.k_stride, p.Hk, p.L, p.dk);
+  fill_strides(p.v_stride, p.H, p.L, p.dv);
+  fill_strides(p.d_out_stride, p.H, p.L, p.dv);
+  fill_strides(p.g_stride, p.H, p.L, 1);
+  fill_strides(p.beta_stride, p.H, p.L, 1);
+  if (!fits(p.q_stride, p.B, p.Hk, p.L) || !fits(p.k_stride, p.B, p.Hk, p.L) || !fits(p.v_stride, p.B, p.H, p.L) ||
+      !fits(p.d_out_stride, p.B, p.H, p.L) || !fits(p.g_stride, p.B, p.H, p.L) || !fits(p.beta_stride, p.B, p.H, p.L))
+    return INFINI_ERR_INVALID_ARG;
+  const bool f32 = (p.mode & INFINI_F32) != 0;
+  const size_t es = f32 ? 4 : 2, tok = (size_t)p.B * p.L, nS = (size_t)p.B * p.H * p.dk * p.dv * 4;
+  struct Range {
+    const void* p;
+    size_t n;
+  };
+  const Range ins[9] = {{p.q, extent(p.q_stride, p.B, p.Hk, p.L, p.dk, es)}, {p.k, extent(p.k_stride, p.B, p.Hk, p.L, p.dk, es)},
+                        {p.v, extent(p.v_stride, p.B, p.H, p.L, p.dv, es)},  {p.d_out, extent(p.d_out_stride, p.B, p.H, p.L, p.dv, es)},
+                        {p.g, extent(p.g_stride, p.B, p.H, p.L, 1, 4)},      {p.beta, extent(p.beta_stride, p.B, p.H, p.L, 1, 4)},
+                        {p.S0, p.S0 ? nS : 0}, {p.dS_L, p.dS_L ? nS : 0},    {p.lens, p.lens ? (size_t)p.B * 4 : 0}};
+  const Range outs[6] = {{p.dq, tok * p.Hk * p.dk * es}, {p.dk_out, tok * p.Hk * p.dk * es}, {p.dv_out, tok * p.H * p.dv * es},
+                         {p.dg, tok * p.H * 4},          {p.dbeta, tok * p.H * 4},           {p.dS0, p.dS0 ? nS : 0}};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& x : ins)
+      if (x.p && outs[i].p && ranges_overlap(outs[i].p, outs[i].n, x.p, x.n)) return INFINI_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; ++j)
+      if (outs[i].p && outs[j].p && ranges_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return INFINI_ERR_INVALID_ARG;
+  }
+  const long long n = all_chunks(shape);
+  const ChunkSpace space(shape, n, true);
+  if (!space_ok(p.workspace, p.workspace_bytes, space.bytes)) return INFINI_ERR_WORKSPACE;
+  rc = check_device(false);
+  if (rc != INFINI_OK) return rc;
+  void* w = p.workspace;
+  if (!w && !ws_alloc(&w, space.bytes, p.stream)) return INFINI_ERR_WORKSPACE;
+  ChunkArgs a = {};
+  a.q = p.q; a.k = p.k; a.v = p.v; a.g = p.g; a.beta = p.beta; a.lens = p.lens; a.d_out = p.d_out; a.S0 = p.S0; a.dS = p.dS_L;
+  a.dq = p.dq; a.dkk = p.dk_out; a.dvv = p.dv_out; a.dg = p.dg; a.dbeta = p.dbeta; a.dS0 = p.dS0;
+  memcpy(a.qs, p.q_stride, sizeof(a.qs));
+  memcpy(a.ks, p.k_stride, sizeof(a.ks));
+  memcpy(a.vs, p.v_stride, sizeof(a.vs));
+  memcpy(a.os, p.d_out_stride, sizeof(a.os));
+  memcpy(a.gs, p.g_stride, sizeof(a.gs));
+  memcpy(a.bs, p.beta_stride, sizeof(a.bs));
+  a.L = p.L; a.B = p.B; a.H = p.H; a.Hk = p.Hk; a.group = p.H / p.Hk; a.dk = p.dk; a.dv = p.dv;
+  a.scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)p.dk);
+  a.vec_k = rows_vec(p.q, p.q_stride, p.dk, es) && rows_vec(p.k, p.k_stride, p.dk, es);
+  a.vec_v = rows_vec(p.v, p.v_stride, p.dv, es);
+  a.vec_o = rows_vec(p.d_out, p.d_out_stride, p.dv, es);
+  a.nc = (int)n;
+  space.place(a, w);
+  const bool wide = padded_dk(p.dk) == 128;
+  rc = f32 ? wide ? chunk_backward<float, 128>(a, p.stream) : chunk_backward<float, 64>(a, p.stream)
+           : wide ? chunk_backward<bf16, 128>(a, p.stream) : chunk_backward<bf16, 64>(a, p.stream);
+  if (!p.workspace && cudaFreeAsync(w, p.stream) != cudaSuccess && rc == INFINI_OK) rc = INFINI_ERR_WORKSPACE;
+  return rc;
 }
 
 int step(const infini_attn_gated_delta_step_params& p) {
@@ -170,8 +370,20 @@ int infini_attn_gated_delta_forward(const infini_attn_gated_delta_params* p) {
 }
 
 size_t infini_attn_gated_delta_workspace_size(const infini_attn_gated_delta_params* p) {
-  (void)p;
-  return 0;
+  if (!p) return 0;
+  const gd::Shape s{p->B, p->H, p->Hk, p->dk, p->dv, p->mode, p->L};
+  if (gd::check_shape(s) != INFINI_OK || p->L < gd::kChunkFrom) return 0;
+  return gd::ChunkSpace(s, gd::slab_chunks(s), false).bytes;
+}
+
+int infini_attn_gated_delta_backward(const infini_attn_gated_delta_backward_params* p) {
+  return p ? gd::backward(*p) : INFINI_ERR_INVALID_ARG;
+}
+
+size_t infini_attn_gated_delta_backward_workspace_size(const infini_attn_gated_delta_backward_params* p) {
+  if (!p) return 0;
+  const gd::Shape s{p->B, p->H, p->Hk, p->dk, p->dv, p->mode, p->L};
+  return gd::check_shape(s) == INFINI_OK ? gd::ChunkSpace(s, gd::all_chunks(s), true).bytes : 0;
 }
 
 int infini_attn_gated_delta_step(const infini_attn_gated_delta_step_params* p) {
@@ -179,7 +391,10 @@ int infini_attn_gated_delta_step(const infini_attn_gated_delta_step_params* p) {
 }
 
 size_t infini_attn_gated_delta_params_size(int which) {
-  return which == 0 ? sizeof(infini_attn_gated_delta_params) : which == 1 ? sizeof(infini_attn_gated_delta_step_params) : 0;
+  return which == 0   ? sizeof(infini_attn_gated_delta_params)
+         : which == 1 ? sizeof(infini_attn_gated_delta_step_params)
+         : which == 2 ? sizeof(infini_attn_gated_delta_backward_params)
+                      : 0;
 }
 
 }  // extern "C"

@@ -1,0 +1,888 @@
+// Gated delta rule over chunks of 64 tokens.
+//
+// With G the running sum of the log decays inside a chunk, gamma_i = e^G_i, rho_i = e^(G_last - G_i),
+// Gamma = e^G_last and S the state before the chunk, the recurrence of 64 tokens is
+//   (I + A) U = X,   A_ij = beta_i e^(G_i - G_j) k_i.k_j (i > j),   X = beta (V - gamma (K S))
+//   O  = scale (gamma (Q S) + P U),   P_ij = e^(G_i - G_j) q_i.k_j (i >= j)
+//   S' = Gamma S + K^T (rho U)
+// prep_kernel computes T = (I + A)^-1 and P of every chunk in parallel; state_kernel passes the
+// state from chunk to chunk.  Only differences G_i - G_j with i >= j enter an exponential, so
+// nothing overflows that the recurrence itself does not.  G is summed in 64 bits (a difference of
+// two sums near -100 would have lost 1e-5 in 32), from max(g, -1e4): e^-1e4 is 0 in fp32, and
+// differences stay finite where g is -inf.
+//
+// Gradients, with d denoting the loss's derivative and dS' that of the state after the chunk:
+//   dU = scale P^T dO + rho (K dS'),  dX = T^T dU,  dV = beta dX,  dA = -dX U^T,  dP = scale dO U^T
+//   dQ = (dP e^(G_i-G_j)) K + scale gamma dO S^T
+//   dK = (dP e^..)^T Q + (M + M^T) K - beta gamma dX S^T + rho U dS'^T,  M_ij = beta_i e^(G_i-G_j) dA_ij
+//   dbeta_i = dX_i.(V - gamma K S)_i + sum_j dA_ij e^(G_i-G_j) k_i.k_j
+//   dG collects every exponent's derivative; dg_t = sum_(i >= t) dG_i
+//   dS = Gamma dS' + scale Q^T (gamma dO) - K^T (beta gamma dX)
+// bwd_state_kernel passes dS from chunk to chunk, grad_kernel does the rest for all chunks in
+// parallel from the stored states and state gradients.
+//
+// Every product runs on mma.sync with fp32 operands split into bf16 parts (gd_frag.cuh).  A warp
+// owns 16 columns of the state, transposed (rows = value columns), in its accumulators: K S, T X,
+// P U and the state's update chain from registers to registers, and nothing crosses warps.
+#pragma once
+
+#include "gd_frag.cuh"
+
+namespace infini {
+namespace gd {
+
+constexpr int kC = 64;             // tokens per chunk
+constexpr int kTri = 10 * 256;     // floats of a lower triangular 64 x 64 matrix: 16 x 16 blocks r >= c at r (r + 1) / 2 + c
+constexpr int kVec = 256;          // floats per chunk: gamma[64], rho[64], beta[64], Gamma
+constexpr int kLdT = 68;           // leading dimension of 64 x 64 fp32 matrices in shared memory
+constexpr int kMaxWarps = 8;
+constexpr float kMinLog = -1e4f;
+
+template <typename T, int DK> struct Dims {
+  static constexpr int kLdK = DK + 16 / (int)sizeof(T);  // rows shifted by 4 banks
+  static constexpr int kIn = sizeof(T) == 2 ? 1 : 3;     // parts of an input element
+  static constexpr int kOut = sizeof(T) == 2 ? 2 : 3;    // parts of an fp32 factor of a result that is rounded to T
+};
+
+struct ChunkArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const void* d_out;
+  const int* lens;
+  long long qs[3], ks[3], vs[3], os[3], gs[3], bs[3];  // os: out, or d_out
+  long long L;
+  int B, H, Hk, group, dk, dv;
+  float scale;
+  bool vec_k, vec_v, vec_o;  // 16-byte rows of q and k, of v, of out / d_out
+  // chunks c0 .. c0 + nc - 1 of every row are worked on; workspaces hold those
+  int c0, nc;
+  int wpc;  // state kernels: warps of a block that own 16 value columns each (a power of 2); the others only load
+  float* T;      // [B H][nc][kTri]
+  float* P;      // [B H][nc][kTri]
+  float* vec;    // [B H][nc][kVec]
+  double* G;     // [B H][nc][64]
+  float4* snap;  // [B H][nc][nw][DK / 8][32]: states before the chunks (accumulator order)
+  float4* dsnap; // the same of the gradients of the states after them
+  float* S;      // state_kernel: [B, H, dk, dv] read and written; grad: unused
+  void* out;
+  const float* S0;  // bwd: initial values, may be null (zero)
+  const float* dS;  // bwd: gradient of the final state, may be null
+  float* dS0;       // bwd: gradient of the initial state, may be null
+  void* dq;
+  void* dkk;
+  void* dvv;
+  float* dg;
+  float* dbeta;
+  float* acc;  // grad, group > 1: [B Hk][nc][2][64][DK] running sums over the value heads of a key head
+};
+
+__device__ __forceinline__ long long row_len(const ChunkArgs& a, int b) {
+  return a.lens ? min(max((long long)a.lens[b], 0LL), a.L) : a.L;
+}
+// valid tokens of chunk c (absolute) of a row of n tokens
+__device__ __forceinline__ int chunk_len(long long n, long long c) { return (int)min(max(n - c * kC, 0LL), (long long)kC); }
+__device__ __forceinline__ int tri_block(int r, int c) { return r * (r + 1) / 2 + c; }
+
+// Lower triangular matrix from its blocks into shared memory [64][kLdT]; blocks above the
+// diagonal are not written.
+__device__ __forceinline__ void load_tri(float* dst, const float* src, int tid, int nthr) {
+  for (int i = tid; i < kTri / 4; i += nthr) {
+    const int blk = i >> 6, e = (i & 63) * 4;
+    const int r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, c = blk - r * (r + 1) / 2;
+    cp_async16(dst + (16 * r + (e >> 4)) * kLdT + 16 * c + (e & 15), src + i * 4, true);
+  }
+}
+
+// ------------------------------------------------------------------ prep
+template <typename T, int DK> struct PrepSmem {
+  T k[kC * Dims<T, DK>::kLdK];
+  T q[kC * Dims<T, DK>::kLdK];
+  float A[kC * kLdT];
+  float R[kC * kLdT];  // T
+  float E[6 * 256];
+  double G[kC];
+  float beta[kC];
+};
+
+template <typename T, int DK> __global__ void __launch_bounds__(256) prep_kernel(const ChunkArgs a) {
+  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  PrepSmem<T, DK>& s = *reinterpret_cast<PrepSmem<T, DK>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group;
+  const long long c = a.c0 + (int)blockIdx.x;
+  const int n = chunk_len(row_len(a, b), c);
+  if (n == 0) return;
+  const long long t0 = c * kC;
+  const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1] + t0 * a.qs[2];
+  const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1] + t0 * a.ks[2];
+  load_rows<T>(s.k, LD, k, a.ks[2], n, a.dk, DK, a.vec_k, tid, 256);
+  load_rows<T>(s.q, LD, q, a.qs[2], n, a.dk, DK, a.vec_k, tid, 256);
+  cp_async_commit();
+  const long long at = ((long long)b * a.H + h) * a.nc + blockIdx.x;
+  if (warp == 0) {
+    const float* gp = a.g + b * a.gs[0] + h * a.gs[1] + t0 * a.gs[2];
+    const float* bp = a.beta + b * a.bs[0] + h * a.bs[1] + t0 * a.bs[2];
+    double x[2];
+    float be[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      const float gt = t < n ? gp[t * a.gs[2]] : 0.f;
+      x[i] = gt < kMinLog ? kMinLog : gt;
+      be[i] = t < n ? bp[t * a.bs[2]] : 0.f;
+    }
+    double sum = x[0] + x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const double G0 = sum - x[1], G1 = sum, last = __shfl_sync(0xffffffffu, sum, 31);
+    s.G[2 * lane] = G0;
+    s.G[2 * lane + 1] = G1;
+    s.beta[2 * lane] = be[0];
+    s.beta[2 * lane + 1] = be[1];
+    *reinterpret_cast<double2*>(a.G + at * kC + 2 * lane) = make_double2(G0, G1);
+    float* v = a.vec + at * kVec;
+    *reinterpret_cast<float2*>(v + 2 * lane) = make_float2(expf((float)G0), expf((float)G1));
+    *reinterpret_cast<float2*>(v + 64 + 2 * lane) = make_float2(expf((float)(last - G0)), expf((float)(last - G1)));
+    *reinterpret_cast<float2*>(v + 128 + 2 * lane) = make_float2(be[0], be[1]);
+    if (lane == 0) v[192] = expf((float)last);
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // warps 0-3: K K^T, warps 4-7: Q K^T, 16 rows each, column blocks up to the diagonal
+  const int rb = warp & 3, m0 = 16 * rb;
+  const bool is_q = warp >= 4;
+  float acc[4][2][4] = {};
+  for (int kk = 0; kk < DK / 16; ++kk) {
+    const AFrag<PI> fa = load_a_k<PI>(is_q ? s.q : s.k, LD, m0, 16 * kk, lane);
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb)
+      if (cb <= rb) mma2(acc[cb][0], acc[cb][1], fa, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
+  }
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb)
+    if (cb <= rb)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int i = m0 + g + 8 * e2, j = 16 * cb + 8 * t + c2;
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool in = is_q ? i >= j + e : i > j + e;
+            x[e] = in ? acc[cb][t][2 * e2 + e] * expf((float)(s.G[i] - s.G[j + e])) * (is_q ? 1.f : s.beta[i]) : 0.f;
+          }
+          if (is_q)
+            *reinterpret_cast<float2*>(a.P + at * kTri + tri_block(rb, cb) * 256 + (g + 8 * e2) * 16 + 8 * t + c2) =
+                make_float2(x[0], x[1]);
+          else
+            *reinterpret_cast<float2*>(s.A + i * kLdT + j) = make_float2(x[0], x[1]);
+        }
+  __syncthreads();
+  // T = (I + A)^-1, lower triangular with a unit diagonal.  Diagonal blocks: column j of block d
+  // by forward substitution, one thread each.
+  if (tid < 64) {
+    const int d = tid >> 4, j = tid & 15;
+    const float* Ad = s.A + 16 * d * kLdT + 16 * d;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float y = i == j ? 1.f : 0.f;
+#pragma unroll
+      for (int m = 0; m < i; ++m) y = fmaf(-Ad[i * kLdT + m], x[m], y);
+      x[i] = i >= j ? y : 0.f;
+      s.R[(16 * d + i) * kLdT + 16 * d + j] = x[i];
+    }
+  }
+  __syncthreads();
+  // off the diagonal, by distance: T_rc = -T_rr (sum_(c <= m < r) A_rm T_mc)
+  for (int d = 1; d < 4; ++d) {
+    const int blocks = 4 - d, i = (tid >> 4) & 15, j = tid & 15;
+    float y[3] = {};
+#pragma unroll
+    for (int cb = 0; cb < 3; ++cb)
+      if (cb < blocks) {
+        const int r = cb + d;
+        for (int m = 16 * cb; m < 16 * r; ++m) y[cb] = fmaf(s.A[(16 * r + i) * kLdT + m], s.R[m * kLdT + 16 * cb + j], y[cb]);
+        s.E[cb * 256 + i * 16 + j] = y[cb];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int cb = 0; cb < 3; ++cb)
+      if (cb < blocks) {
+        const int r = cb + d;
+        float x = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) x = fmaf(-s.R[(16 * r + i) * kLdT + 16 * r + m], s.E[cb * 256 + m * 16 + j], x);
+        s.R[(16 * r + i) * kLdT + 16 * cb + j] = x;
+      }
+    __syncthreads();
+  }
+  float* T_out = a.T + at * kTri;
+  for (int i = tid; i < kTri / 4; i += 256) {
+    const int blk = i >> 6, e = (i & 63) * 4;
+    const int r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, cb = blk - r * (r + 1) / 2;
+    *reinterpret_cast<float4*>(T_out + i * 4) =
+        *reinterpret_cast<const float4*>(s.R + (16 * r + (e >> 4)) * kLdT + 16 * cb + (e & 15));
+  }
+}
+
+// ------------------------------------------------------------------ state
+template <typename T, int DK> struct StateSmem {
+  T k[kC * Dims<T, DK>::kLdK];
+  T q[kC * Dims<T, DK>::kLdK];
+  T v[kC * (16 * kMaxWarps + 16 / sizeof(T))];  // value columns of the block: v, then out; or d_out
+  float Tm[kC * kLdT];
+  float P[kC * kLdT];
+  float vec[kVec];
+};
+template <typename T> constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+
+// S^T fragment of a warp from (to) a [dk, dv] matrix
+template <int DK> __device__ __forceinline__ void state_load(float (&S)[DK / 8][4], const float* p, int v0, int dk, int dv, int lane) {
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+#pragma unroll
+  for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
+      S[n][e] = (p && r < dk && x < dv) ? p[(long long)r * dv + x] : 0.f;
+    }
+}
+template <int DK> __device__ __forceinline__ void state_store(const float (&S)[DK / 8][4], float* p, int v0, int dk, int dv, int lane) {
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+#pragma unroll
+  for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
+      if (r < dk && x < dv) p[(long long)r * dv + x] = S[n][e];
+    }
+}
+
+// One block: wpc x 16 value columns of one (b, h), over all its chunks.  OUT: outputs
+// are computed and the final state goes back to S; otherwise the states before the chunks go to snap.
+template <typename T, int DK, bool OUT> __global__ void __launch_bounds__(32 * kMaxWarps) state_kernel(const ChunkArgs a) {
+  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut, NS = kStages<T>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  StateSmem<T, DK>* sm = reinterpret_cast<StateSmem<T, DK>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int wpc = a.wpc, ldv = 16 * wpc + 16 / (int)sizeof(T), nw = (a.dv + 15) >> 4;
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group;
+  const int wg = warp < wpc ? blockIdx.x * wpc + warp : nw;  // 16 columns from v0
+  const int v0 = 16 * wg, vb = 16 * blockIdx.x * wpc;
+  const long long len = row_len(a, b), bh = (long long)b * a.H + h;
+  const int nc = (int)min((long long)a.nc, max(0LL, (len + kC - 1) / kC - a.c0));
+  if (nc == 0) return;
+  const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1];
+  const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
+  const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + vb;
+  T* out = OUT ? static_cast<T*>(a.out) + b * a.os[0] + h * a.os[1] + vb : nullptr;
+  auto fetch = [&](int i) {
+    StateSmem<T, DK>& s = sm[i % NS];
+    const long long t0 = ((long long)a.c0 + i) * kC, at = bh * a.nc + i;
+    const int n = chunk_len(len, a.c0 + i);
+    load_rows<T>(s.k, LD, k + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
+    load_rows<T>(s.v, ldv, v + t0 * a.vs[2], a.vs[2], n, a.dv - vb, 16 * wpc, a.vec_v, tid, blockDim.x);
+    load_tri(s.Tm, a.T + at * kTri, tid, blockDim.x);
+    if (OUT) {
+      load_rows<T>(s.q, LD, q + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
+      load_tri(s.P, a.P + at * kTri, tid, blockDim.x);
+    }
+    for (int x = tid; x < kVec / 4; x += blockDim.x) cp_async16(s.vec + 4 * x, a.vec + at * kVec + 4 * x, true);
+    cp_async_commit();
+  };
+  float S[DK / 8][4];
+  state_load<DK>(S, OUT ? a.S + bh * a.dk * a.dv : a.S0 ? a.S0 + bh * a.dk * a.dv : nullptr, v0, a.dk, a.dv, lane);
+  fetch(0);
+  for (int i = 0; i < nc; ++i) {
+    if (NS == 2 && i + 1 < nc) {
+      fetch(i + 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    StateSmem<T, DK>& s = sm[i % NS];
+    if (wg < nw) {
+      if (!OUT) {
+        float4* p = a.snap + ((bh * a.nc + i) * nw + wg) * (DK / 8) * 32 + lane;
+#pragma unroll
+        for (int n = 0; n < DK / 8; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
+      }
+      // R^T = S^T K^T, Y^T = S^T Q^T
+      float R[8][4] = {}, Y[8][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        const AFrag<3> fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
+        AFrag<PO> fo;
+        if (OUT)
+#pragma unroll
+          for (int p = 0; p < PO; ++p)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) fo.r[p][x] = fs.r[p][x];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          mma2(R[2 * np], R[2 * np + 1], fs, load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane));
+          if (OUT) mma2(Y[2 * np], Y[2 * np + 1], fo, load_b_k<PI>(s.q, LD, 16 * np, 16 * kk, lane));
+        }
+      }
+      // X^T = beta (V^T - gamma R^T), in R's place
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 8 * n + c2 + (e & 1);
+          R[n][e] = s.vec[128 + t] * (to_f32(s.v[t * ldv + 16 * warp + g + 8 * (e >> 1)]) - s.vec[t] * R[n][e]);
+        }
+      // U^T = X^T T^T
+      float U[8][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<3> fx = from_acc<3>(R[2 * kk], R[2 * kk + 1]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np >= kk) mma2(U[2 * np], U[2 * np + 1], fx, load_b_k<3>(s.Tm, kLdT, 16 * np, 16 * kk, lane));
+      }
+      if (OUT) {
+        // O^T = scale (gamma Y^T + U^T P^T)
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Y[n][e] *= s.vec[8 * n + c2 + (e & 1)];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const AFrag<PO> fu = from_acc<PO>(U[2 * kk], U[2 * kk + 1]);
+#pragma unroll
+          for (int np = 0; np < 4; ++np)
+            if (np >= kk) mma2(Y[2 * np], Y[2 * np + 1], fu, load_b_k<PO>(s.P, kLdT, 16 * np, 16 * kk, lane));
+        }
+        __syncwarp();  // every lane has taken its v
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s.v[(8 * n + c2 + (e & 1)) * ldv + 16 * warp + g + 8 * (e >> 1)] = from_f32<T>(a.scale * Y[n][e]);
+        __syncwarp();
+        const int n = chunk_len(len, a.c0 + i), w = min(16, a.dv - v0);
+        T* o = out + ((long long)a.c0 + i) * kC * a.os[2] + 16 * warp;
+        if (a.vec_o) {
+          constexpr int V = 16 / sizeof(T), per = 16 / V;
+          for (int x = lane; x < kC * per; x += 32) {
+            const int t = x / per, y = (x % per) * V;
+            if (t < n && y < w) *reinterpret_cast<uint4*>(o + t * a.os[2] + y) = *reinterpret_cast<const uint4*>(s.v + t * ldv + 16 * warp + y);
+          }
+        } else {
+          for (int x = lane; x < kC * 16; x += 32) {
+            const int t = x >> 4, y = x & 15;
+            if (t < n && y < w) o[t * a.os[2] + y] = s.v[t * ldv + 16 * warp + y];
+          }
+        }
+      }
+      // S^T = Gamma S^T + (rho U)^T K
+      const float full = s.vec[192];
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] *= full;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[n][e] *= s.vec[64 + 8 * n + c2 + (e & 1)];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np)
+          mma2(S[2 * np], S[2 * np + 1], fu, load_b_n<PI>(s.k, LD, 16 * kk, 16 * np, lane));
+      }
+    }
+    __syncthreads();
+    if (NS == 1 && i + 1 < nc) fetch(i + 1);
+  }
+  if (OUT && wg < nw) state_store<DK>(S, a.S + bh * a.dk * a.dv, v0, a.dk, a.dv, lane);
+}
+
+// The gradient of the state from the last chunk to the first, 16 value columns per warp.
+template <typename T, int DK> __global__ void __launch_bounds__(32 * kMaxWarps) bwd_state_kernel(const ChunkArgs a) {
+  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, NS = kStages<T>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  StateSmem<T, DK>* sm = reinterpret_cast<StateSmem<T, DK>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int wpc = a.wpc, ldv = 16 * wpc + 16 / (int)sizeof(T), nw = (a.dv + 15) >> 4;
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group;
+  const int wg = warp < wpc ? blockIdx.x * wpc + warp : nw, v0 = 16 * wg, vb = 16 * blockIdx.x * wpc;
+  const long long len = row_len(a, b), bh = (long long)b * a.H + h;
+  const int nc = (int)min((long long)a.nc, (len + kC - 1) / kC);
+  const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1];
+  const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
+  const T* d_out = static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + vb;
+  auto fetch = [&](int i) {
+    StateSmem<T, DK>& s = sm[i % NS];
+    const long long t0 = (long long)i * kC, at = bh * a.nc + i;
+    const int n = chunk_len(len, i);
+    load_rows<T>(s.k, LD, k + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
+    load_rows<T>(s.q, LD, q + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
+    load_rows<T>(s.v, ldv, d_out + t0 * a.os[2], a.os[2], n, a.dv - vb, 16 * wpc, a.vec_o, tid, blockDim.x);
+    load_tri(s.Tm, a.T + at * kTri, tid, blockDim.x);
+    load_tri(s.P, a.P + at * kTri, tid, blockDim.x);
+    for (int x = tid; x < kVec / 4; x += blockDim.x) cp_async16(s.vec + 4 * x, a.vec + at * kVec + 4 * x, true);
+    cp_async_commit();
+  };
+  float S[DK / 8][4];
+  state_load<DK>(S, a.dS ? a.dS + bh * a.dk * a.dv : nullptr, v0, a.dk, a.dv, lane);
+  if (nc > 0) fetch(nc - 1);
+  for (int i = nc - 1; i >= 0; --i) {
+    if (NS == 2 && i > 0) {
+      fetch(i - 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    StateSmem<T, DK>& s = sm[i % NS];
+    if (wg < nw) {
+      float4* p = a.dsnap + ((bh * a.nc + i) * nw + wg) * (DK / 8) * 32 + lane;
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
+      // dU^T = scale dO^T P + rho (dS^T K^T)
+      float U[8][4] = {}, W[8][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        const AFrag<3> fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) mma2(W[2 * np], W[2 * np + 1], fs, load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane));
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<PI> fd = load_a_m<PI>(s.v, ldv, 16 * kk, 16 * warp, lane);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np <= kk) mma2(U[2 * np], U[2 * np + 1], fd, load_b_n<3>(s.P, kLdT, 16 * kk, 16 * np, lane));
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          U[n][e] = a.scale * U[n][e] + s.vec[64 + 8 * n + c2 + (e & 1)] * W[n][e];
+          W[n][e] = 0.f;
+        }
+      // dX^T = dU^T T, then -beta gamma dX^T
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np <= kk) mma2(W[2 * np], W[2 * np + 1], fu, load_b_n<3>(s.Tm, kLdT, 16 * kk, 16 * np, lane));
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 8 * n + c2 + (e & 1);
+          W[n][e] *= -s.vec[128 + t] * s.vec[t];
+        }
+      const float full = s.vec[192];
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] *= full;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<3> fx = from_acc<3>(W[2 * kk], W[2 * kk + 1]);
+        const AFrag<3> fd = load_a_m_scaled<3>(s.v, ldv, 16 * kk, 16 * warp, lane, s.vec + 16 * kk, a.scale);
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np) {
+          mma2(S[2 * np], S[2 * np + 1], fx, load_b_n<PI>(s.k, LD, 16 * kk, 16 * np, lane));
+          mma2(S[2 * np], S[2 * np + 1], fd, load_b_n<PI>(s.q, LD, 16 * kk, 16 * np, lane));
+        }
+      }
+    }
+    __syncthreads();
+    if (NS == 1 && i > 0) fetch(i - 1);
+  }
+  if (a.dS0 && wg < nw) state_store<DK>(S, a.dS0 + bh * a.dk * a.dv, v0, a.dk, a.dv, lane);
+}
+
+// ------------------------------------------------------------------ gradients
+constexpr int kLdU = 132;
+template <typename T, int DK> struct GradSmem {
+  T k[kC * Dims<T, DK>::kLdK];
+  T q[kC * Dims<T, DK>::kLdK];
+  T d[kC * Dims<T, 128>::kLdK];  // d_out
+  float U[kC * kLdU];
+  float X[kC * kLdU];  // dX
+  float Tm[kC * kLdT];  // T, then M + M^T
+  float P[kC * kLdT];   // P, then N = dP e^(G_i - G_j)
+  float vec[kVec];
+  double G[kC];
+  float tok[kMaxWarps][3][kC];
+  float rowP[kC], rowA[kC], rowB[kC];
+  float col[kMaxWarps][kC];
+  float sdot[kMaxWarps];
+};
+
+// Sum over the rows of a warp's [16 x 64] fragment: token values x[2 n + e] to dst[64].
+__device__ __forceinline__ void sum_rows(float (&x)[16], float* dst, int lane) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  if (lane < 4)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dst[8 * (i >> 1) + 2 * lane + (i & 1)] = x[i];
+}
+
+// B fragment [k = value column][n = key row] of the state whose accumulator-order copy of the
+// 16 value columns is p.
+template <int P> __device__ __forceinline__ BFrag<P> load_b_state(const float* p, int n0, int lane) {
+  BFrag<P> b;
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* x = p + (((n0 >> 3) + t) * 32 + (2 * c) * 4 + (g >> 1)) * 4 + 2 * h + (g & 1);
+      split<P>(x[0], x[16], b.r, 2 * t + h);
+    }
+  return b;
+}
+
+template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel(const ChunkArgs a) {
+  constexpr int LD = Dims<T, DK>::kLdK, LDD = Dims<T, 128>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  GradSmem<T, DK>& s = *reinterpret_cast<GradSmem<T, DK>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int b = blockIdx.z, hk = blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int i0 = blockIdx.x;
+  const long long t0 = (long long)i0 * kC;
+  const int n = chunk_len(row_len(a, b), i0);
+  const int rows = chunk_len(a.L, i0);  // rows of the tensors in this chunk
+  T* dq = static_cast<T*>(a.dq) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
+  T* dkk = static_cast<T*>(a.dkk) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
+  const T zero = from_f32<T>(0.f);
+  if (n == 0) {  // padding only
+    for (int x = tid; x < rows * a.dk; x += 256) dq[x] = dkk[x] = zero;
+    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
+      const long long r0 = ((long long)b * a.H + h) * a.L + t0;
+      for (int x = tid; x < rows * a.dv; x += 256) static_cast<T*>(a.dvv)[r0 * a.dv + x] = zero;
+      if (tid < rows) a.dg[r0 + tid] = a.dbeta[r0 + tid] = 0.f;
+    }
+    return;
+  }
+  load_rows<T>(s.k, LD, static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1] + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, 256);
+  load_rows<T>(s.q, LD, static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1] + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, 256);
+  for (int hi = 0; hi < a.group; ++hi) {
+    const int h = hk * a.group + hi;
+    const long long bh = (long long)b * a.H + h, at = bh * a.nc + i0, r0 = bh * a.L + t0;
+    load_rows<T>(s.d, LDD, static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + t0 * a.os[2], a.os[2], n, a.dv, 128, a.vec_o, tid, 256);
+    load_tri(s.Tm, a.T + at * kTri, tid, 256);
+    load_tri(s.P, a.P + at * kTri, tid, 256);
+    if (tid < kVec / 4) cp_async16(s.vec + 4 * tid, a.vec + at * kVec + 4 * tid, true);
+    if (tid < kC / 2) cp_async16(s.G + 2 * tid, a.G + at * kC + 2 * tid, true);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    const float4* snap = a.snap + at * nw * (DK / 8) * 32;
+    const float4* dsnap = a.dsnap + at * nw * (DK / 8) * 32;
+    // ---- 1: U, dX and the sums over value columns; 16 value columns per warp
+    if (warp < nw) {
+      float R[8][4] = {}, Y[8][4] = {}, W[8][4] = {}, dot = 0.f;
+      const float4* ps = snap + warp * (DK / 8) * 32 + lane;
+      const float4* pd = dsnap + warp * (DK / 8) * 32 + lane;
+#pragma unroll 2
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        const float4 s0 = ps[2 * kk * 32], s1 = ps[(2 * kk + 1) * 32], d0 = pd[2 * kk * 32], d1 = pd[(2 * kk + 1) * 32];
+        dot += s0.x * d0.x + s0.y * d0.y + s0.z * d0.z + s0.w * d0.w + s1.x * d1.x + s1.y * d1.y + s1.z * d1.z + s1.w * d1.w;
+        const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
+        const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
+        const AFrag<3> fs = from_acc<3>(sa, sb), fd = from_acc<3>(da, db);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          const BFrag<PI> bk = load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane);
+          mma2(R[2 * np], R[2 * np + 1], fs, bk);
+          mma2(W[2 * np], W[2 * np + 1], fd, bk);
+          mma2(Y[2 * np], Y[2 * np + 1], fs, load_b_k<PI>(s.q, LD, 16 * np, 16 * kk, lane));
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) s.sdot[warp] = dot;
+      const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + t0 * a.vs[2] + 16 * warp;
+      const int w = a.dv - 16 * warp;
+      // a_i = scale gamma dO.Y; then Y = V - gamma R (the error the write corrects), R stays K S
+      float sum_a[16];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 8 * x + c2 + e;
+          sum_a[2 * x + e] = a.scale * s.vec[t] *
+                             (to_f32(s.d[t * LDD + 16 * warp + g]) * Y[x][e] + to_f32(s.d[t * LDD + 16 * warp + g + 8]) * Y[x][2 + e]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float vv = (t < n && g + 8 * r < w) ? to_f32(v[t * a.vs[2] + g + 8 * r]) : 0.f;
+            Y[x][2 * r + e] = vv - s.vec[t] * R[x][2 * r + e];
+          }
+        }
+      float U[8][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        float xa[4], xb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          xa[e] = s.vec[128 + 16 * kk + c2 + (e & 1)] * Y[2 * kk][e];
+          xb[e] = s.vec[128 + 16 * kk + 8 + c2 + (e & 1)] * Y[2 * kk + 1][e];
+        }
+        const AFrag<3> fx = from_acc<3>(xa, xb);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np >= kk) mma2(U[2 * np], U[2 * np + 1], fx, load_b_k<3>(s.Tm, kLdT, 16 * np, 16 * kk, lane));
+      }
+      float sum_e[16];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 8 * x + c2 + e;
+          sum_e[2 * x + e] = s.vec[64 + t] * (W[x][e] * U[x][e] + W[x][2 + e] * U[x][2 + e]);
+          s.U[t * kLdU + 16 * warp + g] = U[x][e];
+          s.U[t * kLdU + 16 * warp + g + 8] = U[x][2 + e];
+          U[x][e] = U[x][2 + e] = 0.f;
+        }
+      sum_rows(sum_e, s.tok[warp][1], lane);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<PI> fd = load_a_m<PI>(s.d, LDD, 16 * kk, 16 * warp, lane);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np <= kk) mma2(U[2 * np], U[2 * np + 1], fd, load_b_n<3>(s.P, kLdT, 16 * kk, 16 * np, lane));
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          U[x][e] = a.scale * U[x][e] + s.vec[64 + 8 * x + c2 + (e & 1)] * W[x][e];
+          W[x][e] = 0.f;
+        }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          if (np <= kk) mma2(W[2 * np], W[2 * np + 1], fu, load_b_n<3>(s.Tm, kLdT, 16 * kk, 16 * np, lane));
+      }
+      float sum_b[16];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 8 * x + c2 + e;
+          sum_a[2 * x + e] -= s.vec[128 + t] * s.vec[t] * (W[x][e] * R[x][e] + W[x][2 + e] * R[x][2 + e]);
+          sum_b[2 * x + e] = W[x][e] * Y[x][e] + W[x][2 + e] * Y[x][2 + e];
+          s.X[t * kLdU + 16 * warp + g] = W[x][e];
+          s.X[t * kLdU + 16 * warp + g + 8] = W[x][2 + e];
+        }
+      sum_rows(sum_a, s.tok[warp][0], lane);
+      sum_rows(sum_b, s.tok[warp][2], lane);
+    }
+    __syncthreads();
+    // ---- 2: dP (warps 0-3) and dA (warps 4-7), 16 rows each; dV
+    {
+      T* dv = static_cast<T*>(a.dvv) + r0 * a.dv;
+      for (int x = tid; x < rows * a.dv; x += 256) {
+        const int t = x / a.dv, y = x % a.dv;
+        dv[x] = t < n ? from_f32<T>(s.vec[128 + t] * s.X[t * kLdU + y]) : zero;
+      }
+      const int rb = warp & 3, m0 = 16 * rb;
+      const bool is_a = warp >= 4;
+      float acc[4][2][4] = {}, kk2[4][2][4] = {};
+      for (int kk = 0; kk < nw; ++kk) {
+        AFrag<3> fx;
+        AFrag<PI> fd;
+        if (is_a)
+          fx = load_a_k<3>(s.X, kLdU, m0, 16 * kk, lane);
+        else
+          fd = load_a_k<PI>(s.d, LDD, m0, 16 * kk, lane);
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb)
+          if (cb <= rb) {
+            const BFrag<3> fu = load_b_k<3>(s.U, kLdU, 16 * cb, 16 * kk, lane);
+            if (is_a)
+              mma2(acc[cb][0], acc[cb][1], fx, fu);
+            else
+              mma2(acc[cb][0], acc[cb][1], fd, fu);
+          }
+      }
+      if (is_a)
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          const AFrag<PI> fk = load_a_k<PI>(s.k, LD, m0, 16 * kk, lane);
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb)
+            if (cb <= rb) mma2(kk2[cb][0], kk2[cb][1], fk, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
+        }
+      float row[2] = {}, rowb[2] = {};
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float col[2] = {};
+          const int j = 16 * cb + 8 * t + c2;
+          if (cb <= rb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
+              const float x = acc[cb][t][e];
+              if (is_a) {
+                const float dec = i > jj ? expf((float)(s.G[i] - s.G[jj])) : 0.f, be = s.vec[128 + i];
+                const float ab = -x * dec * kk2[cb][t][e];
+                rowb[e >> 1] += ab;
+                row[e >> 1] += be * ab;
+                col[e & 1] += be * ab;
+                const float m = -x * be * dec;
+                if (i >= jj) s.Tm[i * kLdT + jj] = m;
+                if (i > jj) s.Tm[jj * kLdT + i] = m;
+              } else {
+                const float dp = a.scale * x, y = i >= jj ? dp * s.P[i * kLdT + jj] : 0.f;
+                row[e >> 1] += y;
+                col[e & 1] += y;
+                s.P[i * kLdT + jj] = i >= jj ? dp * expf((float)(s.G[i] - s.G[jj])) : 0.f;
+              }
+            }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            col[0] += __shfl_xor_sync(0xffffffffu, col[0], o);
+            col[1] += __shfl_xor_sync(0xffffffffu, col[1], o);
+          }
+          if (lane < 4) {
+            s.col[warp][j] = col[0];
+            s.col[warp][j + 1] = col[1];
+          }
+        }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          row[r] += __shfl_xor_sync(0xffffffffu, row[r], o);
+          rowb[r] += __shfl_xor_sync(0xffffffffu, rowb[r], o);
+        }
+      if ((lane & 3) == 0)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          (is_a ? s.rowA : s.rowP)[m0 + g + 8 * r] = row[r];
+          if (is_a) s.rowB[m0 + g + 8 * r] = rowb[r];
+        }
+    }
+    __syncthreads();
+    // ---- 3: dg, dbeta (warp 0, two tokens a lane); dQ and dK, 16 key columns per warp
+    if (warp == 0) {
+      double x[2];
+      double sum_e = 0.;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        float av = 0.f, ev = 0.f, bv = 0.f, cv = 0.f;
+        for (int w = 0; w < nw; ++w) {
+          av += s.tok[w][0][t];
+          ev += s.tok[w][1][t];
+          bv += s.tok[w][2][t];
+        }
+        for (int w = 0; w < 8; ++w) cv += s.col[w][t];
+        x[i] = (double)av - ev + s.rowP[t] + s.rowA[t] - cv;
+        sum_e += ev;
+        if (t < rows) a.dbeta[r0 + t] = t < n ? bv + s.rowB[t] : 0.f;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) sum_e += __shfl_xor_sync(0xffffffffu, sum_e, o);
+      float dot = 0.f;
+      for (int w = 0; w < nw; ++w) dot += s.sdot[w];
+      if (lane == 31) x[1] += sum_e + (double)s.vec[192] * dot;
+      double sum = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += y;
+      }
+      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)sum : 0.f;
+      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum - x[0]) : 0.f;
+    }
+    if (warp < DK / 16) {
+      const int n0 = 16 * warp;
+      float Q[4][2][4] = {}, K[4][2][4] = {};
+      for (int kw = 0; kw < nw; ++kw) {
+        const BFrag<PO> fs = load_b_state<PO>(reinterpret_cast<const float*>(snap + kw * (DK / 8) * 32), n0, lane);
+        const BFrag<PO> fd = load_b_state<PO>(reinterpret_cast<const float*>(dsnap + kw * (DK / 8) * 32), n0, lane);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          const int t = 16 * mt + g;
+          mma2(Q[mt][0], Q[mt][1], load_a_k<PI>(s.d, LDD, 16 * mt, 16 * kw, lane), fs);
+          mma2(K[mt][0], K[mt][1],
+               load_a_k<PO>(s.X, kLdU, 16 * mt, 16 * kw, lane, -s.vec[128 + t] * s.vec[t], -s.vec[136 + t] * s.vec[t + 8]), fs);
+          mma2(K[mt][0], K[mt][1], load_a_k<PO>(s.U, kLdU, 16 * mt, 16 * kw, lane, s.vec[64 + t], s.vec[72 + t]), fd);
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Q[mt][t][e] *= a.scale * s.vec[16 * mt + g + 8 * (e >> 1)];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const BFrag<PI> bk = load_b_n<PI>(s.k, LD, 16 * kk, n0, lane), bq = load_b_n<PI>(s.q, LD, 16 * kk, n0, lane);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          if (kk <= mt) mma2(Q[mt][0], Q[mt][1], load_a_k<PO>(s.P, kLdT, 16 * mt, 16 * kk, lane), bk);
+          mma2(K[mt][0], K[mt][1], load_a_k<PO>(s.Tm, kLdT, 16 * mt, 16 * kk, lane), bk);
+          if (kk >= mt) mma2(K[mt][0], K[mt][1], load_a_m<PO>(s.P, kLdT, 16 * kk, 16 * mt, lane), bq);
+        }
+      }
+      float* acc = a.acc + (((long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int tk = 16 * mt + g + 8 * r, x = n0 + 8 * t + c2;
+            float2 yq = make_float2(Q[mt][t][2 * r], Q[mt][t][2 * r + 1]), yk = make_float2(K[mt][t][2 * r], K[mt][t][2 * r + 1]);
+            if (a.group > 1) {  // the same thread holds this element for every value head of the key head
+              float2* pq = reinterpret_cast<float2*>(acc + tk * DK + x);
+              float2* pk = reinterpret_cast<float2*>(acc + (kC + tk) * DK + x);
+              if (hi > 0) {
+                const float2 oq = *pq, ok = *pk;
+                yq.x += oq.x; yq.y += oq.y; yk.x += ok.x; yk.y += ok.y;
+              }
+              if (hi + 1 < a.group) {
+                *pq = yq;
+                *pk = yk;
+                continue;
+              }
+            }
+            if (tk < rows) {
+              const long long o = (long long)tk * a.dk + x;
+              const bool in = tk < n;
+              if (x < a.dk) {
+                dq[o] = in ? from_f32<T>(yq.x) : zero;
+                dkk[o] = in ? from_f32<T>(yk.x) : zero;
+              }
+              if (x + 1 < a.dk) {
+                dq[o + 1] = in ? from_f32<T>(yq.y) : zero;
+                dkk[o + 1] = in ? from_f32<T>(yk.y) : zero;
+              }
+            }
+          }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace gd
+}  // namespace infini

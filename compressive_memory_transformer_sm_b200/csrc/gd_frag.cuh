@@ -1,0 +1,215 @@
+// Warp-level pieces of the chunked gated delta rule: mma.sync fragments of
+// bf16 products whose fp32 operands are split into bf16 parts.
+//
+// An fp32 x is b1 + b2 + b3 with b1 = bf16(x), b2 = bf16(x - b1), b3 = bf16(x - b1 - b2): three
+// parts keep its 24 bits, two about 16.  A product of operands with PA and PB parts sums the
+// pairs whose order i + j stays below max(PA, PB): 3 products for an fp32 operand with an exact
+// bf16 one, 6 for two fp32 operands (relative 2^-24), 3 for two of two parts (2^-16).
+//
+// Fragments of m16n8k16, lane = 4 g + c:  A holds rows g, g + 8 and k = 2c, 2c + 1, 2c + 8, 2c + 9;
+// B the same k of column g; the accumulator rows g, g + 8 of columns 2c, 2c + 1.  The
+// accumulators of two neighbouring column tiles are therefore an A fragment of the next product.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace infini {
+namespace gd {
+
+typedef __nv_bfloat16 bf16;
+
+template <int P> struct AFrag {
+  uint32_t r[P][4];
+};
+template <int P> struct BFrag {  // two column tiles: [2 t + h], k half h of tile t
+  uint32_t r[P][4];
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Column tiles 0, 1 of d += A B.  The smallest terms first.
+template <int PA, int PB> __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const AFrag<PA>& a, const BFrag<PB>& b) {
+  constexpr int M = (PA > PB ? PA : PB) - 1;
+#pragma unroll
+  for (int o = M; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int j = o - i;
+      if (j < 0 || j >= PB) continue;
+      mma16816(d0, a.r[i], b.r[j][0], b.r[j][1]);
+      mma16816(d1, a.r[i], b.r[j][2], b.r[j][3]);
+    }
+}
+
+// Slot s of every part from the pair (x0, x1).
+template <int P> __device__ __forceinline__ void split(float x0, float x1, uint32_t (&r)[P][4], int s) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t h = pack_bf16x2(x0, x1);
+    r[p][s] = h;
+    if (p + 1 < P) {
+      x0 -= bf16_lo(h);
+      x1 -= bf16_hi(h);
+    }
+  }
+}
+// A fragment of k-step kk from accumulator tiles, each column (= k) times s.
+template <int P> __device__ __forceinline__ AFrag<P> from_acc(const float (&lo)[4], const float (&hi)[4]) {
+  AFrag<P> a;
+  split<P>(lo[0], lo[1], a.r, 0);
+  split<P>(lo[2], lo[3], a.r, 1);
+  split<P>(hi[0], hi[1], a.r, 2);
+  split<P>(hi[2], hi[3], a.r, 3);
+  return a;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const bf16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const bf16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+
+// B[k][n] = m[n][k] (k contiguous), columns n0 .. n0 + 15.
+template <int P> __device__ __forceinline__ BFrag<P> load_b_k(const bf16* m, int ld, int n0, int k0, int lane) {
+  static_assert(P == 1, "bf16 is exact in one part");
+  BFrag<P> b;
+  ldsm4(b.r[0], m + (n0 + (lane >> 4) * 8 + (lane & 7)) * ld + k0 + ((lane >> 3) & 1) * 8);
+  return b;
+}
+template <int P> __device__ __forceinline__ BFrag<P> load_b_k(const float* m, int ld, int n0, int k0, int lane) {
+  BFrag<P> b;
+  const float* p = m + (n0 + (lane >> 2)) * ld + k0 + 2 * (lane & 3);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = *reinterpret_cast<const float2*>(p + 8 * t * ld + 8 * h);
+      split<P>(x.x, x.y, b.r, 2 * t + h);
+    }
+  return b;
+}
+// B[k][n] = m[k][n] (n contiguous).
+template <int P> __device__ __forceinline__ BFrag<P> load_b_n(const bf16* m, int ld, int k0, int n0, int lane) {
+  static_assert(P == 1, "bf16 is exact in one part");
+  BFrag<P> b;
+  ldsm4t(b.r[0], m + (k0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * ld + n0 + (lane >> 4) * 8);
+  return b;
+}
+template <int P> __device__ __forceinline__ BFrag<P> load_b_n(const float* m, int ld, int k0, int n0, int lane) {
+  BFrag<P> b;
+  const float* p = m + (k0 + 2 * (lane & 3)) * ld + n0 + (lane >> 2);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) split<P>(p[8 * h * ld + 8 * t], p[(8 * h + 1) * ld + 8 * t], b.r, 2 * t + h);
+  return b;
+}
+// A[m][k] = x[m][k] (k contiguous).
+template <int P> __device__ __forceinline__ AFrag<P> load_a_k(const bf16* x, int ld, int m0, int k0, int lane) {
+  static_assert(P == 1, "bf16 is exact in one part");
+  AFrag<P> a;
+  ldsm4(a.r[0], x + (m0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * ld + k0 + (lane >> 4) * 8);
+  return a;
+}
+// ... of an fp32 operand, rows g and g + 8 times s0 and s1
+template <int P>
+__device__ __forceinline__ AFrag<P> load_a_k(const float* x, int ld, int m0, int k0, int lane, float s0 = 1.f, float s1 = 1.f) {
+  AFrag<P> a;
+  const float* p = x + (m0 + (lane >> 2)) * ld + k0 + 2 * (lane & 3);
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) {
+      const float2 v = *reinterpret_cast<const float2*>(p + 8 * rh * ld + 8 * kh);
+      const float s = rh ? s1 : s0;
+      split<P>(s * v.x, s * v.y, a.r, rh + 2 * kh);
+    }
+  return a;
+}
+// A[m][k] = x[k][m] (m contiguous).
+template <int P> __device__ __forceinline__ AFrag<P> load_a_m(const bf16* x, int ld, int k0, int m0, int lane) {
+  static_assert(P == 1, "bf16 is exact in one part");
+  AFrag<P> a;
+  ldsm4t(a.r[0], x + (k0 + (lane >> 4) * 8 + (lane & 7)) * ld + m0 + ((lane >> 3) & 1) * 8);
+  return a;
+}
+template <int P> __device__ __forceinline__ AFrag<P> load_a_m(const float* x, int ld, int k0, int m0, int lane) {
+  AFrag<P> a;
+  const float* p = x + (k0 + 2 * (lane & 3)) * ld + m0 + (lane >> 2);
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) split<P>(p[8 * kh * ld + 8 * rh], p[(8 * kh + 1) * ld + 8 * rh], a.r, rh + 2 * kh);
+  return a;
+}
+// ... with k times s[k] (s at k0), in P parts
+template <int P> __device__ __forceinline__ AFrag<P> load_a_m_scaled(const bf16* x, int ld, int k0, int m0, int lane, const float* s, float f) {
+  const AFrag<1> e = load_a_m<1>(x, ld, k0, m0, lane);
+  AFrag<P> a;
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh) {
+    const float2 w = *reinterpret_cast<const float2*>(s + 8 * kh + 2 * (lane & 3));
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) {
+      const uint32_t u = e.r[0][rh + 2 * kh];
+      split<P>(bf16_lo(u) * (f * w.x), bf16_hi(u) * (f * w.y), a.r, rh + 2 * kh);
+    }
+  }
+  return a;
+}
+template <int P> __device__ __forceinline__ AFrag<P> load_a_m_scaled(const float* x, int ld, int k0, int m0, int lane, const float* s, float f) {
+  AFrag<P> a;
+  const float* p = x + (k0 + 2 * (lane & 3)) * ld + m0 + (lane >> 2);
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh) {
+    const float2 w = *reinterpret_cast<const float2*>(s + 8 * kh + 2 * (lane & 3));
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh)
+      split<P>(p[8 * kh * ld + 8 * rh] * (f * w.x), p[(8 * kh + 1) * ld + 8 * rh] * (f * w.y), a.r, rh + 2 * kh);
+  }
+  return a;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;  // the rest is written as zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows 0 .. 63 of `cols` (a multiple of 16 bytes) elements into shared memory, zeros where the
+// row is at or past n or the column at or past d.  vec: rows start on 16 bytes and d is a
+// multiple of them; then the copy is asynchronous.
+template <typename T>
+__device__ __forceinline__ void load_rows(T* dst, int ld, const T* src, long long stride, int n, int d, int cols, bool vec,
+                                          int tid, int nthr) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {
+    const int per = cols / V, rows = nthr / per, x = (tid % per) * V;  // nthr is a multiple of per
+    for (int r = tid / per; r < 64; r += rows) {
+      const bool in = r < n && x < d;
+      cp_async16(dst + r * ld + x, in ? src + r * stride + x : src, in);
+    }
+  } else {
+    for (int i = tid; i < 64 * cols; i += nthr) {
+      const int r = i / cols, x = i % cols;
+      dst[r * ld + x] = (r < n && x < d) ? src[r * stride + x] : from_f32<T>(0.f);
+    }
+  }
+}
+
+}  // namespace gd
+}  // namespace infini

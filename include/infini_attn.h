@@ -382,6 +382,45 @@ INFINI_API int infini_attn_gated_delta_forward(const infini_attn_gated_delta_par
 INFINI_API size_t infini_attn_gated_delta_workspace_size(const infini_attn_gated_delta_params* p);
 
 /*
+ * Gradients of a loss through the forward: from d_out = dLoss/d out and (optional) dS_L = dLoss/d S_L, the state
+ * after the last token, to dq, dk [B, Hk, L, dk] (summed over the value heads of a key head), dv [B, H, L, dv] (the
+ * inputs' type), dg, dbeta [B, H, L] fp32 and (optional) dS0 [B, H, dk, dv] fp32; every output contiguous and
+ * overlapping nothing else.  S0 is the state the forward started from (NULL: zero), dS_L NULL: zero.  d_out has
+ * strides of its own.
+ */
+typedef struct infini_attn_gated_delta_backward_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const float* S0;
+  const void* d_out;
+  const float* dS_L;
+  const int* lens;
+  void* dq;
+  void* dk_out;
+  void* dv_out;
+  float* dg;
+  float* dbeta;
+  float* dS0;
+  int B, H, Hk;
+  long long L;
+  int dk, dv;
+  int mode;
+  float scale;
+  long long q_stride[3], k_stride[3], v_stride[3], d_out_stride[3], g_stride[3], beta_stride[3];
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+} infini_attn_gated_delta_backward_params;
+
+INFINI_API int infini_attn_gated_delta_backward(const infini_attn_gated_delta_backward_params* p);
+
+/* Bytes of workspace the backward needs (0 if the shape is invalid). */
+INFINI_API size_t infini_attn_gated_delta_backward_workspace_size(const infini_attn_gated_delta_backward_params* p);
+
+/*
  * One token of B requests (serving): q_t, k_t [B, Hk, dk], v_t, out [B, H, dv], g, beta [B, H]; strides of
  * (B, head), all zero selects the contiguous layout.  S [pool, H, dk, dv] fp32 is a pool of states: request b
  * owns row slots[b] (device, int32; NULL: row b, and pool >= B), updated in place.  A slot outside [0, pool) is a

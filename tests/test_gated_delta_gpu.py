@@ -238,3 +238,132 @@ def test_streams_workspaces_and_graphs():
     if n:
         with pytest.raises(api.InfiniAttnError):
             api.infini_attn_gated_delta_forward(q, k, v, g, beta, S0.clone(), out, workspace=ws[:n - 256])
+
+
+def check_backward(x, d_out, dS, got, scale=0.0, lens=None):
+    q, k, v, g, beta, S0 = x
+    n = None if lens is None else lens.tolist()
+    z = torch.zeros(q.shape[0], v.shape[1], q.shape[3], v.shape[3], device=DEV)
+    want = G.backward(*map(np64, (q, k, v, g, beta, z if S0 is None else S0, d_out, z if dS is None else dS)),
+                      scale or q.shape[-1] ** -0.5, n)
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), got, want):
+        if a is not None:
+            try:
+                near(a, w)
+            except AssertionError as e:
+                raise AssertionError(f"{name}: {e}") from None
+
+
+def backward_inputs(B, H, Hk, L, dk, dv, t, seed=0):
+    x = make(B, H, Hk, L, dk, dv, t, seed)
+    gen = torch.Generator(device=DEV).manual_seed(seed + 99)
+    return x, torch.randn(B, H, L, dv, generator=gen, device=DEV).to(t), 0.3 * torch.randn(B, H, dk, dv, generator=gen, device=DEV)
+
+
+@pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,L,dk,dv", [s for s in SHAPES if s[3] < 1000] + [(1, 1, 1, 500, 128, 128)])
+def test_backward(B, H, Hk, L, dk, dv, t):
+    x, d_out, dS = backward_inputs(B, H, Hk, L, dk, dv, t)
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS)
+    check_backward(x, d_out, dS, got)
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, want_state_grad=False, scale=0.25)
+    assert got[5] is None
+    check_backward((*x[:5], None), d_out, None, got, scale=0.25)
+
+
+@pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
+def test_backward_lens(t):
+    x, d_out, dS = backward_inputs(6, 4, 2, 200, 128, 48, t)
+    lens = torch.tensor([0, 1, 64, 199, 300, -5], dtype=torch.int32, device=DEV)
+    dirty = [y.clone() for y in (*x[:5], d_out)]
+    for b, n in enumerate(lens.tolist()):
+        for y in dirty:
+            y[b, :, min(max(n, 0), 200):] = float("nan")
+    got = api.infini_attn_gated_delta_backward(*dirty, S0=x[5], dS_L=dS, lens=lens)
+    check_backward(x, d_out, dS, got, lens=lens)
+    for y in got[:5]:
+        for b, n in enumerate(lens.tolist()):
+            assert not y[b, :, min(max(n, 0), 200):].any()
+    assert torch.equal(got[5][0], dS[0])
+
+
+@pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
+def test_backward_strides_and_decays(t):
+    x, d_out, dS = backward_inputs(2, 3, 1, 150, 40, 24, t, seed=2)
+    q, k, v, g, beta, S0 = x
+    g[:, 0] = 0
+    g[:, 1, ::9] = float("-inf")
+    g[:, 2, 70:] = -1e30
+    beta[:, 1, 3:9] = 0
+    turn = lambda y: y.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    d2 = d_out[:, :1].expand(2, 3, 150, 24)
+    got = api.infini_attn_gated_delta_backward(turn(q), turn(k), turn(v), turn(g), turn(beta), d2, S0=S0, dS_L=dS)
+    check_backward(x, d2, dS, got)
+
+
+def test_backward_against_differences():
+    """The loss's change along a random direction, from the forward's own fp32 outputs: truncation about eps^2 = 1e-4
+    relative and cancellation 2e-6 / 1e-2 = 2e-4 of the loss's terms; 5e-3 holds both."""
+    x, d_out, dS = backward_inputs(1, 4, 2, 130, 64, 64, FP, seed=8)
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    for i, (y, dy) in enumerate(zip(x, got)):
+        d = torch.randn(y.shape, generator=gen, device=DEV) * y.abs().mean()
+        ends = []
+        for e in (1e-2, -1e-2):
+            z = list(x)
+            z[i] = y + e * d
+            out, S = forward(*z)
+            ends.append(float((out.double() * d_out).sum() + (S.double() * dS).sum()))
+        slope, size = (dy.double() * d).sum().item(), (dy.double() * d).norm().item()
+        assert abs((ends[0] - ends[1]) / 2e-2 - slope) <= 5e-3 * max(abs(slope), size), i
+
+
+def test_backward_streams_workspaces_and_graphs():
+    x, d_out, dS = backward_inputs(2, 4, 2, 333, 128, 128, BF, seed=12)
+    call = lambda **kw: api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS, **kw)  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    n = api.infini_attn_gated_delta_backward_workspace_size(2, 4, 2, 333, 128, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    got = call(workspace=ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph, held = torch.cuda.CUDAGraph(), None
+    with torch.cuda.graph(graph):
+        held = call(workspace=ws)
+    for _ in range(2):
+        for y in held:
+            y.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, want))
+    with pytest.raises(api.InfiniAttnError):
+        call(workspace=ws[:n - 256])
+
+
+def test_norm_memory_and_gradients_together():
+    """One layer's pass as a model runs it: norm, q and k of unit length, gated delta rule, and back through both."""
+    B, H, L, D = 2, 4, 150, 512
+    gen = torch.Generator(device=DEV).manual_seed(31)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    x, w, bias = r(B, L, D).to(BF), (1 + 0.1 * r(D)).to(BF), (0.1 * r(D)).to(BF)
+    y = torch.empty_like(x)
+    api.infini_attn_layer_norm_forward(x, w, bias, y)
+    v = y.view(B, L, H, 128).transpose(1, 2)  # the normalised rows are the values, heads side by side
+    q, k, _, g, beta, S0 = make(B, H, H, L, 128, 128, seed=4)
+    out, S = torch.empty(B, H, L, 128, dtype=BF, device=DEV), S0.clone()
+    api.infini_attn_gated_delta_forward(q, k, v, g, beta, S, out)
+    d_out = r(B, H, L, 128).to(BF)
+    grads = api.infini_attn_gated_delta_backward(q, k, v, g, beta, d_out, S0=S0)
+    d_y = grads[2].transpose(1, 2).reshape(B, L, D)
+    dx, dw, db = api.infini_attn_layer_norm_backward(x, w, d_y)
+    wo, wS = G.forward(*map(np64, (q, k, v, g, beta, S0)), 128 ** -0.5)
+    near(out, wo)
+    near(S, wS)
+    check_backward((q, k, v, g, beta, S0), d_out, None, grads)
+    wx, ww, wb = G.layer_norm_backward(*map(np64, (x, w, d_y)), 1e-5)
+    near(dx, wx)
+    near(dw, ww)
+    near(db, wb)

@@ -39,9 +39,24 @@ pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host pointers
 
 
 def test_struct_sizes():
-    for which, cls in enumerate((api.GatedDeltaParams, api.GatedDeltaStepParams)):
+    for which, cls in enumerate((api.GatedDeltaParams, api.GatedDeltaStepParams, api.GatedDeltaBackwardParams)):
         assert api.lib.infini_attn_gated_delta_params_size(which) == ctypes.sizeof(cls)
     assert api.lib.infini_attn_gated_delta_params_size(7) == 0
+
+
+def backward_params(**over):
+    p = api.GatedDeltaBackwardParams()
+    names = ("q", "k", "v", "g", "beta", "S0", "d_out", "dS_L", "dq", "dk_out", "dv_out", "dg", "dbeta", "dS0")
+    for i, n in enumerate(names):
+        setattr(p, n, host((i + 1) << 16))
+    p.B, p.H, p.Hk, p.L, p.dk, p.dv, p.mode = 1, 2, 1, 4, 16, 8, 0
+    for n, x in over.items():
+        setattr(p, n, x)
+    return p
+
+
+def backward(**over):
+    return api.lib.infini_attn_gated_delta_backward(ctypes.byref(backward_params(**over)))
 
 
 def forward(**over):
@@ -85,6 +100,32 @@ def test_overlaps_are_refused():
 ])
 def test_step_refusals(over, rc):
     assert step(**over) == rc
+
+
+@pytest.mark.parametrize("over,rc", [
+    (dict(), api.INFINI_ERR_DEVICE), (dict(S0=None, dS_L=None, dS0=None), api.INFINI_ERR_DEVICE), (dict(q=None), BAD),
+    (dict(d_out=None), BAD), (dict(dq=None), BAD), (dict(dk_out=None), BAD), (dict(dv_out=None), BAD), (dict(dg=None), BAD),
+    (dict(dbeta=None), BAD), (dict(H=3, Hk=2), BAD), (dict(L=-1), BAD), (dict(dk=129), UNSUP), (dict(mode=1), UNSUP),
+    (dict(d_out_stride=L3(-1, 0, 8)), BAD),
+])
+def test_backward_refusals(over, rc):
+    assert backward(**over) == rc
+
+
+def test_backward_overlaps_and_workspaces():
+    p = backward_params()
+    for out in ("dq", "dk_out", "dv_out", "dg", "dbeta", "dS0"):
+        assert backward(**{out: p.v}) == BAD and backward(**{out: p.S0}) == BAD
+    assert backward(dq=p.dk_out) == BAD and backward(dg=p.dbeta) == BAD and backward(lens=p.dv_out) == BAD
+    n = api.infini_attn_gated_delta_backward_workspace_size(1, 2, 1, 4, 16, 8)
+    ws = host(20 << 16)
+    assert n > 0 and api.infini_attn_gated_delta_backward_workspace_size(1, 3, 2, 4, 16, 8) == 0
+    assert backward(workspace=ws, workspace_bytes=n) == api.INFINI_ERR_DEVICE
+    assert backward(workspace=ws, workspace_bytes=n - 1) == api.INFINI_ERR_WORKSPACE
+    assert backward(workspace=ws + 16, workspace_bytes=n) == api.INFINI_ERR_WORKSPACE
+    m = api.infini_attn_gated_delta_workspace_size(1, 2, 1, 100, 16, 8)
+    assert m > 0 and api.infini_attn_gated_delta_workspace_size(1, 2, 1, 1, 16, 8) == 0
+    assert forward(L=100, workspace=ws, workspace_bytes=m - 1) == api.INFINI_ERR_WORKSPACE
 
 
 def test_layer_norm_refusals():
