@@ -85,6 +85,8 @@ bool rows_vec(const void* p, const long long st[3], int d, size_t es) {
 int padded_dk(int dk) { return dk <= 64 ? 64 : 128; }
 int col_warps(int dv) { return (dv + 15) / 16; }
 
+int out_parts(int mode) { return (mode & INFINI_F32) ? 3 : 2; }
+
 // Workspace of nc chunks of every (b, h).
 struct ChunkSpace {
   size_t T, P, vec, G, snap, dsnap, acc, bytes;
@@ -96,8 +98,8 @@ struct ChunkSpace {
       at += align_up(bytes);
       return was;
     };
-    T = take(n * kTri * 4);
-    P = take(n * kTri * 4);
+    T = take(n * 3 * kTri * 2);
+    P = take(n * (bwd ? 3 : out_parts(s.mode)) * kTri * 2);
     vec = take(n * kVec * 4);
     G = take(n * kC * 8);
     snap = take(bwd ? n * state : 0);
@@ -107,8 +109,8 @@ struct ChunkSpace {
   }
   void place(ChunkArgs& a, void* ws) const {
     char* w = static_cast<char*>(ws);
-    a.T = reinterpret_cast<float*>(w + T);
-    a.P = reinterpret_cast<float*>(w + P);
+    a.T = reinterpret_cast<bf16*>(w + T);
+    a.P = reinterpret_cast<bf16*>(w + P);
     a.vec = reinterpret_cast<float*>(w + vec);
     a.G = reinterpret_cast<double*>(w + G);
     a.snap = reinterpret_cast<float4*>(w + snap);
@@ -121,7 +123,7 @@ struct ChunkSpace {
 constexpr size_t kSlabBytes = size_t(1) << 30;
 long long all_chunks(const Shape& s) { return (s.L + kC - 1) / kC; }
 long long slab_chunks(const Shape& s) {
-  const size_t one = (size_t)s.B * s.H * (2 * kTri * 4 + kVec * 4 + kC * 8);
+  const size_t one = (size_t)s.B * s.H * ((3 + out_parts(s.mode)) * kTri * 2 + kVec * 4 + kC * 8);
   return std::max<long long>(1, std::min<long long>(all_chunks(s), (long long)(kSlabBytes / one)));
 }
 
@@ -138,40 +140,61 @@ template <typename F> int launch_chunk(F* kernel, dim3 grid, int threads, size_t
   return launch_status();
 }
 
-// Warps of a state block: as few as keep the blocks within one per SM, so that few heads spread over many SMs.
-int warps_per_block(int nw, long long heads) {
-  int w = 1;
-  while (w < kMaxWarps && w < nw && heads * ((nw + w - 1) / w) > kSms) w *= 2;
-  return w;
+// Shape of a state block.  KS 4: four warps to 16 value columns, for the shortest time per chunk; KS 1: one warp, less
+// exchange, for the most chunks per SM.  As few groups per block as keep the blocks within one per SM.
+struct StatePlan {
+  int KS, groups, stages, blocks, threads, first_loader;
+  size_t smem;
+};
+template <typename T, int DK, int PP> StatePlan state_plan(int nw, long long heads) {
+  StatePlan p = {};
+  p.KS = heads * nw <= 2 * kSms ? 4 : 1;
+  const int most = p.KS == 4 ? (sizeof(T) == 2 ? 4 : 2) : kMaxGroups;  // what fits in shared memory
+  p.groups = 1;
+  while (p.groups < most && p.groups < nw && heads * ((nw + p.groups - 1) / p.groups) > kSms) p.groups *= 2;
+  p.blocks = (nw + p.groups - 1) / p.groups;
+  const size_t ex = p.KS == 4 ? p.groups * sizeof(Exchange<DK, Dims<T, DK>::kOut>) : 0;
+  p.stages = 2 * stage_bytes<T, DK, PP>(p.groups) + ex <= 232448 ? 2 : 1;
+  p.smem = p.stages * stage_bytes<T, DK, PP>(p.groups) + ex;
+  // four more warps to copy, where the register file has room and the copies would take a large part of a chunk's time
+  const bool loaders = p.KS == 4 ? p.groups < 4 && p.stages == 2 : p.groups == 1;
+  const int work = 32 * p.KS * p.groups;
+  p.first_loader = loaders ? work : 0;
+  p.threads = loaders ? work + 128 : std::max(128, work);
+  return p;
 }
 
-template <typename T, int DK> int run_prep(const ChunkArgs& a, cudaStream_t st) {
-  return launch_chunk(prep_kernel<T, DK>, dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
-}
-template <typename T, int DK, bool OUT> int run_state(ChunkArgs a, cudaStream_t st) {
-  const int nw = col_warps(a.dv);
-  a.wpc = warps_per_block(nw, (long long)a.B * a.H);
-  return launch_chunk(state_kernel<T, DK, OUT>, dim3((nw + a.wpc - 1) / a.wpc, a.H, a.B), std::max(128, 32 * a.wpc),
-                      kStages<T> * sizeof(StateSmem<T, DK>), kPhaseState, a, st);
+template <typename T, int DK, int PP> int run_prep(const ChunkArgs& a, cudaStream_t st) {
+  return launch_chunk(prep_kernel<T, DK, PP>, dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
 }
 template <typename T, int DK> int chunk_forward(ChunkArgs a, long long chunks, long long slab, cudaStream_t st) {
+  constexpr int PP = Dims<T, DK>::kOut;
+  const StatePlan p = state_plan<T, DK, PP>(col_warps(a.dv), (long long)a.B * a.H);
+  a.groups = p.groups;
+  a.stages = p.stages;
+  a.first_loader = p.first_loader;
+  const dim3 grid(p.blocks, a.H, a.B);
   for (long long c = 0; c < chunks; c += slab) {
     a.c0 = (int)c;
     a.nc = (int)std::min(slab, chunks - c);
-    int rc = run_prep<T, DK>(a, st);
-    if (rc == INFINI_OK) rc = run_state<T, DK, true>(a, st);
+    int rc = run_prep<T, DK, PP>(a, st);
+    if (rc == INFINI_OK)
+      rc = p.KS == 4 ? launch_chunk(forward_kernel<T, DK, 4>, grid, p.threads, p.smem, kPhaseState, a, st)
+                     : launch_chunk(forward_kernel<T, DK, 1>, grid, p.threads, p.smem, kPhaseState, a, st);
     if (rc != INFINI_OK) return rc;
   }
   return INFINI_OK;
 }
 template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
-  int rc = run_prep<T, DK>(a, st);
-  if (rc == INFINI_OK) rc = run_state<T, DK, false>(a, st);
+  int rc = run_prep<T, DK, 3>(a, st);
   if (rc != INFINI_OK) return rc;
-  const int nw = col_warps(a.dv);
-  a.wpc = warps_per_block(nw, (long long)a.B * a.H);
-  rc = launch_chunk(bwd_state_kernel<T, DK>, dim3((nw + a.wpc - 1) / a.wpc, a.H, a.B), std::max(128, 32 * a.wpc),
-                    kStages<T> * sizeof(StateSmem<T, DK>), kPhaseBwd, a, st);
+  const StatePlan p = state_plan<T, DK, 3>(col_warps(a.dv), 2LL * a.B * a.H);
+  a.groups = p.groups;
+  a.stages = p.stages;
+  a.first_loader = p.first_loader;
+  const dim3 grid(2 * p.blocks, a.H, a.B);
+  rc = p.KS == 4 ? launch_chunk(both_kernel<T, DK, 4>, grid, p.threads, p.smem, kPhaseBwd, a, st)
+                 : launch_chunk(both_kernel<T, DK, 1>, grid, p.threads, p.smem, kPhaseBwd, a, st);
   if (rc != INFINI_OK) return rc;
   return launch_chunk(grad_kernel<T, DK>, dim3(a.nc, a.Hk, a.B), 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
 }
@@ -359,6 +382,7 @@ int step(const infini_attn_gated_delta_step_params& p) {
 
 }  // namespace
 }  // namespace gd
+
 }  // namespace infini
 
 using namespace infini;

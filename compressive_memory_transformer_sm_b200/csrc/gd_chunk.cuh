@@ -21,9 +21,11 @@
 // bwd_state_kernel passes dS from chunk to chunk, grad_kernel does the rest for all chunks in
 // parallel from the stored states and state gradients.
 //
-// Every product runs on mma.sync with fp32 operands split into bf16 parts (gd_frag.cuh).  A warp
-// owns 16 columns of the state, transposed (rows = value columns), in its accumulators: K S, T X,
-// P U and the state's update chain from registers to registers, and nothing crosses warps.
+// Every product runs on mma.sync with fp32 operands split into bf16 parts (gd_frag.cuh).  A group
+// of KS warps owns 16 columns of the state, transposed (rows = value columns): each warp holds
+// DK / KS rows of S in its accumulators and works on 64 / KS tokens of a chunk, so that K S, T X,
+// P U and the update of S follow one another with fragments that pass through shared memory
+// unchanged (KS 4) or stay in registers (KS 1).
 #pragma once
 
 #include "gd_frag.cuh"
@@ -32,7 +34,7 @@ namespace infini {
 namespace gd {
 
 constexpr int kC = 64;             // tokens per chunk
-constexpr int kTri = 10 * 256;     // floats of a lower triangular 64 x 64 matrix: 16 x 16 blocks r >= c at r (r + 1) / 2 + c
+constexpr int kTri = 10 * 256;     // elements of a lower triangular 64 x 64 matrix: 16 x 16 blocks r >= c at r (r + 1) / 2 + c, swizzled (tri_at)
 constexpr int kVec = 256;          // floats per chunk: gamma[64], rho[64], beta[64], Gamma
 constexpr int kLdT = 68;           // leading dimension of 64 x 64 fp32 matrices in shared memory
 constexpr int kMaxWarps = 8;
@@ -59,9 +61,11 @@ struct ChunkArgs {
   bool vec_k, vec_v, vec_o;  // 16-byte rows of q and k, of v, of out / d_out
   // chunks c0 .. c0 + nc - 1 of every row are worked on; workspaces hold those
   int c0, nc;
-  int wpc;  // state kernels: warps of a block that own 16 value columns each (a power of 2); the others only load
-  float* T;      // [B H][nc][kTri]
-  float* P;      // [B H][nc][kTri]
+  int groups;  // state kernels: groups of 16 value columns per block (a power of 2)
+  int stages;  // ... chunks in shared memory, 1 or 2
+  int first_loader;  // ... the threads from this one on copy the next chunk
+  bf16* T;       // [B H][nc][3][kTri]: the three bf16 parts
+  bf16* P;       // [B H][nc][parts][kTri]
   float* vec;    // [B H][nc][kVec]
   double* G;     // [B H][nc][64]
   float4* snap;  // [B H][nc][nw][DK / 8][32]: states before the chunks (accumulator order)
@@ -86,13 +90,40 @@ __device__ __forceinline__ long long row_len(const ChunkArgs& a, int b) {
 __device__ __forceinline__ int chunk_len(long long n, long long c) { return (int)min(max(n - c * kC, 0LL), (long long)kC); }
 __device__ __forceinline__ int tri_block(int r, int c) { return r * (r + 1) / 2 + c; }
 
-// Lower triangular matrix from its blocks into shared memory [64][kLdT]; blocks above the
-// diagonal are not written.
-__device__ __forceinline__ void load_tri(float* dst, const float* src, int tid, int nthr) {
-  for (int i = tid; i < kTri / 4; i += nthr) {
-    const int blk = i >> 6, e = (i & 63) * 4;
-    const int r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, c = blk - r * (r + 1) / 2;
-    cp_async16(dst + (16 * r + (e >> 4)) * kLdT + 16 * c + (e & 15), src + i * 4, true);
+// Element (r, c) of a 16 x 16 block: 16-byte halves of a row change places every 4 rows, so that 8
+// rows of a half lie in different banks.
+__device__ __forceinline__ int tri_at(int r, int c) { return r * 16 + ((((c >> 3) ^ (r >> 2)) & 1) << 3) + (c & 7); }
+// B[k][n] = m[n][k] of block (rb, cb): n its rows, k its columns; B[k][n] = m[k][n]: the other way.
+template <int P> __device__ __forceinline__ BFrag<P> load_tri_k(const bf16* m, int rb, int cb, int lane) {
+  BFrag<P> b;
+  const bf16* x = m + tri_block(rb, cb) * 256 + tri_at((lane >> 4) * 8 + (lane & 7), lane & 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4(b.r[p], x + p * kTri);
+  return b;
+}
+template <int P> __device__ __forceinline__ BFrag<P> load_tri_n(const bf16* m, int rb, int cb, int lane) {
+  BFrag<P> b;
+  const bf16* x = m + tri_block(rb, cb) * 256 + tri_at((lane & 8) + (lane & 7), (lane >> 4) * 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4t(b.r[p], x + p * kTri);
+  return b;
+}
+// A matrix of three parts as fp32 [64][kLdT].
+__device__ __forceinline__ void load_tri_f32(float* dst, const bf16* src, int tid, int nthr) {
+  for (int i = tid; i < kTri; i += nthr) {
+    const int blk = i >> 8, r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, c = blk - r * (r + 1) / 2;
+    const bf16* x = src + blk * 256 + tri_at((i >> 4) & 15, i & 15);
+    dst[(16 * r + ((i >> 4) & 15)) * kLdT + 16 * c + (i & 15)] = (to_f32(x[2 * kTri]) + to_f32(x[kTri])) + to_f32(x[0]);
+  }
+}
+// The parts of (x0, x1), elements at and at + 1 of planes `plane` apart.
+template <int P> __device__ __forceinline__ void put_parts(bf16* dst, int plane, float x0, float x1) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t h = pack_bf16x2(x0, x1);
+    *reinterpret_cast<uint32_t*>(dst + p * plane) = h;
+    x0 -= bf16_lo(h);
+    x1 -= bf16_hi(h);
   }
 }
 
@@ -107,7 +138,8 @@ template <typename T, int DK> struct PrepSmem {
   float beta[kC];
 };
 
-template <typename T, int DK> __global__ void __launch_bounds__(256) prep_kernel(const ChunkArgs a) {
+// PP: parts of P that are stored
+template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) prep_kernel(const ChunkArgs a) {
   constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   PrepSmem<T, DK>& s = *reinterpret_cast<PrepSmem<T, DK>*>(smem_raw);
@@ -180,8 +212,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) prep_kernel
             x[e] = in ? acc[cb][t][2 * e2 + e] * expf((float)(s.G[i] - s.G[j + e])) * (is_q ? 1.f : s.beta[i]) : 0.f;
           }
           if (is_q)
-            *reinterpret_cast<float2*>(a.P + at * kTri + tri_block(rb, cb) * 256 + (g + 8 * e2) * 16 + 8 * t + c2) =
-                make_float2(x[0], x[1]);
+            put_parts<PP>(a.P + at * PP * kTri + tri_block(rb, cb) * 256 + tri_at(g + 8 * e2, 8 * t + c2), kTri, x[0], x[1]);
           else
             *reinterpret_cast<float2*>(s.A + i * kLdT + j) = make_float2(x[0], x[1]);
         }
@@ -225,59 +256,109 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) prep_kernel
       }
     __syncthreads();
   }
-  float* T_out = a.T + at * kTri;
-  for (int i = tid; i < kTri / 4; i += 256) {
-    const int blk = i >> 6, e = (i & 63) * 4;
+  bf16* T_out = a.T + at * 3 * kTri;
+  for (int i = tid; i < kTri / 2; i += 256) {
+    const int blk = i >> 7, e = (i & 127) * 2;
     const int r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, cb = blk - r * (r + 1) / 2;
-    *reinterpret_cast<float4*>(T_out + i * 4) =
-        *reinterpret_cast<const float4*>(s.R + (16 * r + (e >> 4)) * kLdT + 16 * cb + (e & 15));
+    const float2 x = *reinterpret_cast<const float2*>(s.R + (16 * r + (e >> 4)) * kLdT + 16 * cb + (e & 15));
+    put_parts<3>(T_out + blk * 256 + tri_at(e >> 4, e & 15), kTri, x.x, x.y);
   }
 }
 
 // ------------------------------------------------------------------ state
-template <typename T, int DK> struct StateSmem {
+constexpr int kMaxGroups = 8;
+template <typename T, int DK, int PP> struct Stage {
   T k[kC * Dims<T, DK>::kLdK];
   T q[kC * Dims<T, DK>::kLdK];
-  T v[kC * (16 * kMaxWarps + 16 / sizeof(T))];  // value columns of the block: v, then out; or d_out
-  float Tm[kC * kLdT];
-  float P[kC * kLdT];
+  bf16 Tm[3 * kTri];
+  bf16 P[PP * kTri];
   float vec[kVec];
+  // then [64][ldv] of T: the block's value columns of v (then of out) or d_out
 };
-template <typename T> constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+// Fragments that the warps of a group exchange (KS > 1): of S, of X (dU), of rho U (dX) and of U.
+template <int DK, int PO> struct Exchange {
+  uint4 S[DK / 16][3][32];
+  uint4 X[4][3][32];
+  uint4 W[4][3][32];
+  uint4 U[4][PO][32];
+};
+template <typename T> __host__ __device__ constexpr int strip_ld(int groups) { return 16 * groups + 16 / (int)sizeof(T); }
+template <typename T, int DK, int PP> __host__ __device__ constexpr size_t stage_bytes(int groups) {
+  return sizeof(Stage<T, DK, PP>) + kC * strip_ld<T>(groups) * sizeof(T);
+}
 
-// S^T fragment of a warp from (to) a [dk, dv] matrix
-template <int DK> __device__ __forceinline__ void state_load(float (&S)[DK / 8][4], const float* p, int v0, int dk, int dv, int lane) {
+// A chunk's operands into a stage, by the threads `tid` of `nthr`.
+struct Fetch {
+  const void *k, *q, *x;  // the chunk's first rows; q may be null
+  long long ks, qs, xs;   // row strides
+  int n, dk, w;           // rows, elements of a row of k and q, of x
+  bool vec_k, vec_x;
+  const bf16 *T, *P;      // P may be null
+  const float* vec;
+};
+template <typename T, int DK, int PP>
+__device__ __forceinline__ void fetch_chunk(Stage<T, DK, PP>& s, const Fetch& f, int ldx, int cols, int tid, int nthr) {
+  constexpr int LD = Dims<T, DK>::kLdK;
+  load_rows<T>(s.k, LD, static_cast<const T*>(f.k), f.ks, f.n, f.dk, DK, f.vec_k, tid, nthr);
+  if (f.q) load_rows<T>(s.q, LD, static_cast<const T*>(f.q), f.qs, f.n, f.dk, DK, f.vec_k, tid, nthr);
+  load_rows<T>(reinterpret_cast<T*>(&s + 1), ldx, static_cast<const T*>(f.x), f.xs, f.n, f.w, cols, f.vec_x, tid, nthr);
+#pragma unroll 4
+  for (int i = tid; i < 3 * kTri / 8; i += nthr) cp_async16(s.Tm + 8 * i, f.T + 8 * i, true);
+  if (f.P)
+#pragma unroll 4
+    for (int i = tid; i < PP * kTri / 8; i += nthr) cp_async16(s.P + 8 * i, f.P + 8 * i, true);
+  for (int i = tid; i < kVec / 4; i += nthr) cp_async16(s.vec + 4 * i, f.vec + 4 * i, true);
+  cp_async_commit();
+}
+
+// Rows r0 .. r0 + 8 N - 1 of 16 columns from v0 of a [dk, dv] matrix, transposed.
+template <int N> __device__ __forceinline__ void state_load(float (&S)[N][4], const float* p, int r0, int v0, int dk, int dv, int lane) {
   const int g = lane >> 2, c2 = 2 * (lane & 3);
 #pragma unroll
-  for (int n = 0; n < DK / 8; ++n)
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
+      const int r = r0 + 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
       S[n][e] = (p && r < dk && x < dv) ? p[(long long)r * dv + x] : 0.f;
     }
 }
-template <int DK> __device__ __forceinline__ void state_store(const float (&S)[DK / 8][4], float* p, int v0, int dk, int dv, int lane) {
+template <int N> __device__ __forceinline__ void state_store(const float (&S)[N][4], float* p, int r0, int v0, int dk, int dv, int lane) {
   const int g = lane >> 2, c2 = 2 * (lane & 3);
 #pragma unroll
-  for (int n = 0; n < DK / 8; ++n)
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
+      const int r = r0 + 8 * n + c2 + (e & 1), x = v0 + g + 8 * (e >> 1);
       if (r < dk && x < dv) p[(long long)r * dv + x] = S[n][e];
     }
 }
+template <int N> __device__ __forceinline__ void state_snap(const float (&S)[N][4], float4* p) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
+}
 
-// One block: wpc x 16 value columns of one (b, h), over all its chunks.  OUT: outputs
-// are computed and the final state goes back to S; otherwise the states before the chunks go to snap.
-template <typename T, int DK, bool OUT> __global__ void __launch_bounds__(32 * kMaxWarps) state_kernel(const ChunkArgs a) {
-  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut, NS = kStages<T>;
+// What a group's warps hold and how they meet.
+template <int KS> __device__ __forceinline__ void group_sync(int group) {
+  if constexpr (KS > 1)
+    named_bar_sync(1 + group, 32 * KS);
+  else
+    __syncwarp();
+}
+
+// One block: `groups` x 16 value columns of one (b, h), over all its chunks.  OUT: outputs are
+// computed and the final state goes back to S; otherwise the states before the chunks go to snap.
+template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int h, int b) {
+  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut;
+  constexpr int NB = 4 / KS, ND = DK / KS / 8;  // token blocks and state tiles of a warp
+  typedef Stage<T, DK, PP> St;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  StateSmem<T, DK>* sm = reinterpret_cast<StateSmem<T, DK>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
-  const int wpc = a.wpc, ldv = 16 * wpc + 16 / (int)sizeof(T), nw = (a.dv + 15) >> 4;
-  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group;
-  const int wg = warp < wpc ? blockIdx.x * wpc + warp : nw;  // 16 columns from v0
-  const int v0 = 16 * wg, vb = 16 * blockIdx.x * wpc;
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int group = warp / KS, ks = warp % KS, ldv = strip_ld<T>(a.groups), nw = (a.dv + 15) >> 4;
+  const int wg = group < a.groups ? vblock * a.groups + group : nw;  // 16 columns from v0
+  const int v0 = 16 * wg, vb = 16 * vblock * a.groups, vs = 16 * group;
+  const int hk = h / a.group;
+  const size_t stage = stage_bytes<T, DK, PP>(a.groups);
+  Exchange<DK, PO>& ex = reinterpret_cast<Exchange<DK, PO>*>(smem_raw + a.stages * stage)[KS > 1 ? group : 0];
   const long long len = row_len(a, b), bh = (long long)b * a.H + h;
   const int nc = (int)min((long long)a.nc, max(0LL, (len + kC - 1) / kC - a.c0));
   if (nc == 0) return;
@@ -285,230 +366,336 @@ template <typename T, int DK, bool OUT> __global__ void __launch_bounds__(32 * k
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
   const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + vb;
   T* out = OUT ? static_cast<T*>(a.out) + b * a.os[0] + h * a.os[1] + vb : nullptr;
+  const int w_in = min(16 * a.groups, a.dv - vb);
   auto fetch = [&](int i) {
-    StateSmem<T, DK>& s = sm[i % NS];
+    if (tid < a.first_loader) return;
     const long long t0 = ((long long)a.c0 + i) * kC, at = bh * a.nc + i;
-    const int n = chunk_len(len, a.c0 + i);
-    load_rows<T>(s.k, LD, k + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
-    load_rows<T>(s.v, ldv, v + t0 * a.vs[2], a.vs[2], n, a.dv - vb, 16 * wpc, a.vec_v, tid, blockDim.x);
-    load_tri(s.Tm, a.T + at * kTri, tid, blockDim.x);
-    if (OUT) {
-      load_rows<T>(s.q, LD, q + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
-      load_tri(s.P, a.P + at * kTri, tid, blockDim.x);
-    }
-    for (int x = tid; x < kVec / 4; x += blockDim.x) cp_async16(s.vec + 4 * x, a.vec + at * kVec + 4 * x, true);
-    cp_async_commit();
+    const Fetch f = {k + t0 * a.ks[2], OUT ? q + t0 * a.qs[2] : nullptr, v + t0 * a.vs[2], a.ks[2], a.qs[2], a.vs[2],
+                     chunk_len(len, a.c0 + i), a.dk, w_in, a.vec_k, a.vec_v, a.T + at * 3 * kTri,
+                     OUT ? a.P + at * PP * kTri : nullptr, a.vec + at * kVec};
+    fetch_chunk<T, DK, PP>(*reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage), f, ldv, 16 * a.groups,
+                           tid - a.first_loader, nthr - a.first_loader);
   };
-  float S[DK / 8][4];
-  state_load<DK>(S, OUT ? a.S + bh * a.dk * a.dv : a.S0 ? a.S0 + bh * a.dk * a.dv : nullptr, v0, a.dk, a.dv, lane);
+  const bool live = wg < nw;
+  float S[ND][4];
+  const float* from = OUT ? a.S : a.S0;
+  state_load<ND>(S, from ? from + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
   fetch(0);
   for (int i = 0; i < nc; ++i) {
-    if (NS == 2 && i + 1 < nc) {
-      fetch(i + 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
-    __syncthreads();
-    StateSmem<T, DK>& s = sm[i % NS];
-    if (wg < nw) {
-      if (!OUT) {
-        float4* p = a.snap + ((bh * a.nc + i) * nw + wg) * (DK / 8) * 32 + lane;
+    if constexpr (KS > 1)
+      if (live)
 #pragma unroll
-        for (int n = 0; n < DK / 8; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
-      }
-      // R^T = S^T K^T, Y^T = S^T Q^T
-      float R[8][4] = {}, Y[8][4] = {};
+        for (int kk = 0; kk < ND / 2; ++kk)
+          put_frag<3>(ex.S[ks * (ND / 2) + kk][0], from_acc<3>(S[2 * kk], S[2 * kk + 1]), lane);
+    cp_async_wait<0>();
+    __syncthreads();
+    if (a.stages == 2 && i + 1 < nc) fetch(i + 1);
+    St& s = *reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage);
+    T* sv = reinterpret_cast<T*>(&s + 1);
+    if (live) {
+      if (!OUT) state_snap<ND>(S, a.snap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
+      // R^T = S^T K^T, Y^T = S^T Q^T: 16 tokens per block
+      float R[NB][2][4] = {}, Y[NB][2][4] = {}, lo[NB][2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
-        const AFrag<3> fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
-        AFrag<PO> fo;
-        if (OUT)
+        AFrag<3> fs;
+        if constexpr (KS > 1)
+          fs = get_frag<3>(ex.S[kk][0], lane);
+        else
+          fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
 #pragma unroll
-          for (int p = 0; p < PO; ++p)
+        for (int x = 0; x < NB; ++x) {
+          const int blk = KS > 1 ? ks : x;
+          mma2(R[x][0], R[x][1], lo[x][0], lo[x][1], fs, load_b_k<PI>(s.k, LD, 16 * blk, 16 * kk, lane));
+          if (OUT) {
+            AFrag<PO> fo;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) fo.r[p][x] = fs.r[p][x];
+            for (int p = 0; p < PO; ++p)
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          mma2(R[2 * np], R[2 * np + 1], fs, load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane));
-          if (OUT) mma2(Y[2 * np], Y[2 * np + 1], fo, load_b_k<PI>(s.q, LD, 16 * np, 16 * kk, lane));
+              for (int y = 0; y < 4; ++y) fo.r[p][y] = fs.r[p][y];
+            mma2(Y[x][0], Y[x][1], fo, load_b_k<PI>(s.q, LD, 16 * blk, 16 * kk, lane));
+          }
         }
       }
       // X^T = beta (V^T - gamma R^T), in R's place
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int x = 0; x < NB; ++x) {
+        const int blk = KS > 1 ? ks : x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 8 * n + c2 + (e & 1);
-          R[n][e] = s.vec[128 + t] * (to_f32(s.v[t * ldv + 16 * warp + g + 8 * (e >> 1)]) - s.vec[t] * R[n][e]);
-        }
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 16 * blk + 8 * y + c2 + (e & 1);
+            R[x][y][e] = s.vec[128 + t] * (to_f32(sv[t * ldv + vs + g + 8 * (e >> 1)]) - s.vec[t] * (R[x][y][e] + lo[x][y][e]));
+            lo[x][y][e] = 0.f;
+          }
+        if constexpr (KS > 1) put_frag<3>(ex.X[blk][0], from_acc<3>(R[x][0], R[x][1]), lane);
+      }
+      if constexpr (KS > 1) group_sync<KS>(group);
       // U^T = X^T T^T
-      float U[8][4] = {};
+      float U[NB][2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const AFrag<3> fx = from_acc<3>(R[2 * kk], R[2 * kk + 1]);
+        if (KS > 1 && kk > ks) break;
+        AFrag<3> fx;
+        if constexpr (KS > 1)
+          fx = get_frag<3>(ex.X[kk][0], lane);
+        else
+          fx = from_acc<3>(R[kk][0], R[kk][1]);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-          if (np >= kk) mma2(U[2 * np], U[2 * np + 1], fx, load_b_k<3>(s.Tm, kLdT, 16 * np, 16 * kk, lane));
+        for (int x = 0; x < NB; ++x) {
+          const int blk = KS > 1 ? ks : x;
+          if (KS > 1 || blk >= kk)
+            mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fx, load_tri_k<3>(s.Tm, blk, kk, lane));
+        }
+      }
+      AFrag<3> fw[4];   // rho U
+      AFrag<PO> fu[4];  // U
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        const int blk = KS > 1 ? ks : x;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) U[x][y][e] += lo[x][y][e];
+        if (OUT) {
+          fu[x] = from_acc<PO>(U[x][0], U[x][1]);
+          if constexpr (KS > 1) put_frag<PO>(ex.U[blk][0], fu[x], lane);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) U[x][y][e] *= s.vec[64 + 16 * blk + 8 * y + c2 + (e & 1)];
+        fw[x] = from_acc<3>(U[x][0], U[x][1]);
+        if constexpr (KS > 1) put_frag<3>(ex.W[blk][0], fw[x], lane);
+      }
+      if constexpr (KS > 1) {
+        group_sync<KS>(group);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) fw[kk] = get_frag<3>(ex.W[kk][0], lane);
       }
       if (OUT) {
         // O^T = scale (gamma Y^T + U^T P^T)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int x = 0; x < NB; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) Y[n][e] *= s.vec[8 * n + c2 + (e & 1)];
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Y[x][y][e] *= s.vec[16 * (KS > 1 ? ks : x) + 8 * y + c2 + (e & 1)];
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const AFrag<PO> fu = from_acc<PO>(U[2 * kk], U[2 * kk + 1]);
+          if (KS > 1 && kk > ks) break;
+          if constexpr (KS > 1) fu[kk] = get_frag<PO>(ex.U[kk][0], lane);
 #pragma unroll
-          for (int np = 0; np < 4; ++np)
-            if (np >= kk) mma2(Y[2 * np], Y[2 * np + 1], fu, load_b_k<PO>(s.P, kLdT, 16 * np, 16 * kk, lane));
+          for (int x = 0; x < NB; ++x) {
+            const int blk = KS > 1 ? ks : x;
+            if (KS > 1 || blk >= kk)
+              mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, blk, kk, lane));
+          }
         }
         __syncwarp();  // every lane has taken its v
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s.v[(8 * n + c2 + (e & 1)) * ldv + 16 * warp + g + 8 * (e >> 1)] = from_f32<T>(a.scale * Y[n][e]);
-        __syncwarp();
         const int n = chunk_len(len, a.c0 + i), w = min(16, a.dv - v0);
-        T* o = out + ((long long)a.c0 + i) * kC * a.os[2] + 16 * warp;
+        T* o = out + ((long long)a.c0 + i) * kC * a.os[2] + vs;
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sv[(16 * (KS > 1 ? ks : x) + 8 * y + c2 + (e & 1)) * ldv + vs + g + 8 * (e >> 1)] = from_f32<T>(a.scale * Y[x][y][e]);
+        __syncwarp();
+        const int ta = KS > 1 ? 16 * ks : 0;
         if (a.vec_o) {
           constexpr int V = 16 / sizeof(T), per = 16 / V;
-          for (int x = lane; x < kC * per; x += 32) {
-            const int t = x / per, y = (x % per) * V;
-            if (t < n && y < w) *reinterpret_cast<uint4*>(o + t * a.os[2] + y) = *reinterpret_cast<const uint4*>(s.v + t * ldv + 16 * warp + y);
+#pragma unroll
+          for (int x = lane; x < 16 * NB * per; x += 32) {
+            const int t = ta + x / per, y = (x % per) * V;
+            if (t < n && y < w) *reinterpret_cast<uint4*>(o + t * a.os[2] + y) = *reinterpret_cast<const uint4*>(sv + t * ldv + vs + y);
           }
         } else {
-          for (int x = lane; x < kC * 16; x += 32) {
-            const int t = x >> 4, y = x & 15;
-            if (t < n && y < w) o[t * a.os[2] + y] = s.v[t * ldv + 16 * warp + y];
+          for (int x = lane; x < 16 * NB * 16; x += 32) {
+            const int t = ta + (x >> 4), y = x & 15;
+            if (t < n && y < w) o[t * a.os[2] + y] = sv[t * ldv + vs + y];
           }
         }
       }
       // S^T = Gamma S^T + (rho U)^T K
       const float full = s.vec[192];
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n)
+      for (int np = 0; np < ND / 2; ++np) {
+        float hi[2][4] = {}, lw[2][4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[n][e] *= full;
+        for (int kk = 0; kk < 4; ++kk)
+          mma2(hi[0], hi[1], lw[0], lw[1], fw[kk], load_b_n<PI>(s.k, LD, 16 * kk, ks * (DK / KS) + 16 * np, lane));
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) U[n][e] *= s.vec[64 + 8 * n + c2 + (e & 1)];
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
-#pragma unroll
-        for (int np = 0; np < DK / 16; ++np)
-          mma2(S[2 * np], S[2 * np + 1], fu, load_b_n<PI>(s.k, LD, 16 * kk, 16 * np, lane));
+          for (int e = 0; e < 4; ++e) S[2 * np + y][e] = fmaf(full, S[2 * np + y][e], hi[y][e] + lw[y][e]);
       }
     }
-    __syncthreads();
-    if (NS == 1 && i + 1 < nc) fetch(i + 1);
+    if (a.stages == 1) {
+      __syncthreads();
+      if (i + 1 < nc) fetch(i + 1);
+    }
   }
-  if (OUT && wg < nw) state_store<DK>(S, a.S + bh * a.dk * a.dv, v0, a.dk, a.dv, lane);
+  if (OUT && live) state_store<ND>(S, a.S + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
 }
 
-// The gradient of the state from the last chunk to the first, 16 value columns per warp.
-template <typename T, int DK> __global__ void __launch_bounds__(32 * kMaxWarps) bwd_state_kernel(const ChunkArgs a) {
-  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, NS = kStages<T>;
+// The gradient of the state from the last chunk to the first.
+template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_pass(const ChunkArgs& a, int vblock, int h, int b) {
+  constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut;
+  constexpr int NB = 4 / KS, ND = DK / KS / 8;
+  typedef Stage<T, DK, 3> St;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  StateSmem<T, DK>* sm = reinterpret_cast<StateSmem<T, DK>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
-  const int wpc = a.wpc, ldv = 16 * wpc + 16 / (int)sizeof(T), nw = (a.dv + 15) >> 4;
-  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group;
-  const int wg = warp < wpc ? blockIdx.x * wpc + warp : nw, v0 = 16 * wg, vb = 16 * blockIdx.x * wpc;
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, c2 = 2 * (lane & 3);
+  const int group = warp / KS, ks = warp % KS, ldv = strip_ld<T>(a.groups), nw = (a.dv + 15) >> 4;
+  const int wg = group < a.groups ? vblock * a.groups + group : nw;
+  const int v0 = 16 * wg, vb = 16 * vblock * a.groups, vs = 16 * group;
+  const int hk = h / a.group;
+  const size_t stage = stage_bytes<T, DK, 3>(a.groups);
+  Exchange<DK, PO>& ex = reinterpret_cast<Exchange<DK, PO>*>(smem_raw + a.stages * stage)[KS > 1 ? group : 0];
   const long long len = row_len(a, b), bh = (long long)b * a.H + h;
   const int nc = (int)min((long long)a.nc, (len + kC - 1) / kC);
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1];
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
   const T* d_out = static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + vb;
+  const int w_in = min(16 * a.groups, a.dv - vb);
   auto fetch = [&](int i) {
-    StateSmem<T, DK>& s = sm[i % NS];
+    if (tid < a.first_loader) return;
     const long long t0 = (long long)i * kC, at = bh * a.nc + i;
-    const int n = chunk_len(len, i);
-    load_rows<T>(s.k, LD, k + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
-    load_rows<T>(s.q, LD, q + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, blockDim.x);
-    load_rows<T>(s.v, ldv, d_out + t0 * a.os[2], a.os[2], n, a.dv - vb, 16 * wpc, a.vec_o, tid, blockDim.x);
-    load_tri(s.Tm, a.T + at * kTri, tid, blockDim.x);
-    load_tri(s.P, a.P + at * kTri, tid, blockDim.x);
-    for (int x = tid; x < kVec / 4; x += blockDim.x) cp_async16(s.vec + 4 * x, a.vec + at * kVec + 4 * x, true);
-    cp_async_commit();
+    const Fetch f = {k + t0 * a.ks[2], q + t0 * a.qs[2], d_out + t0 * a.os[2], a.ks[2], a.qs[2], a.os[2], chunk_len(len, i),
+                     a.dk, w_in, a.vec_k, a.vec_o, a.T + at * 3 * kTri, a.P + at * 3 * kTri, a.vec + at * kVec};
+    fetch_chunk<T, DK, 3>(*reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage), f, ldv, 16 * a.groups,
+                          tid - a.first_loader, nthr - a.first_loader);
   };
-  float S[DK / 8][4];
-  state_load<DK>(S, a.dS ? a.dS + bh * a.dk * a.dv : nullptr, v0, a.dk, a.dv, lane);
+  const bool live = wg < nw;
+  float S[ND][4];
+  state_load<ND>(S, a.dS ? a.dS + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
   if (nc > 0) fetch(nc - 1);
   for (int i = nc - 1; i >= 0; --i) {
-    if (NS == 2 && i > 0) {
-      fetch(i - 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
-    __syncthreads();
-    StateSmem<T, DK>& s = sm[i % NS];
-    if (wg < nw) {
-      float4* p = a.dsnap + ((bh * a.nc + i) * nw + wg) * (DK / 8) * 32 + lane;
+    if constexpr (KS > 1)
+      if (live)
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
+        for (int kk = 0; kk < ND / 2; ++kk)
+          put_frag<3>(ex.S[ks * (ND / 2) + kk][0], from_acc<3>(S[2 * kk], S[2 * kk + 1]), lane);
+    cp_async_wait<0>();
+    __syncthreads();
+    if (a.stages == 2 && i > 0) fetch(i - 1);
+    St& s = *reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage);
+    const T* sd = reinterpret_cast<const T*>(&s + 1);
+    if (live) {
+      state_snap<ND>(S, a.dsnap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // dU^T = scale dO^T P + rho (dS^T K^T)
-      float U[8][4] = {}, W[8][4] = {};
+      float U[NB][2][4] = {}, W[NB][2][4] = {}, lo[NB][2][4] = {}, lw[NB][2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
-        const AFrag<3> fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
+        AFrag<3> fs;
+        if constexpr (KS > 1)
+          fs = get_frag<3>(ex.S[kk][0], lane);
+        else
+          fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) mma2(W[2 * np], W[2 * np + 1], fs, load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane));
+        for (int x = 0; x < NB; ++x)
+          mma2(W[x][0], W[x][1], lw[x][0], lw[x][1], fs, load_b_k<PI>(s.k, LD, 16 * (KS > 1 ? ks : x), 16 * kk, lane));
       }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const AFrag<PI> fd = load_a_m<PI>(s.v, ldv, 16 * kk, 16 * warp, lane);
+        if (KS > 1 && kk < ks) continue;
+        const AFrag<PI> fd = load_a_m<PI>(sd, ldv, 16 * kk, vs, lane);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-          if (np <= kk) mma2(U[2 * np], U[2 * np + 1], fd, load_b_n<3>(s.P, kLdT, 16 * kk, 16 * np, lane));
+        for (int x = 0; x < NB; ++x) {
+          const int blk = KS > 1 ? ks : x;
+          if (KS > 1 || blk <= kk)
+            mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fd, load_tri_n<3>(s.P, kk, blk, lane));
+        }
       }
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int x = 0; x < NB; ++x) {
+        const int blk = KS > 1 ? ks : x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          U[n][e] = a.scale * U[n][e] + s.vec[64 + 8 * n + c2 + (e & 1)] * W[n][e];
-          W[n][e] = 0.f;
-        }
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            U[x][y][e] = a.scale * (U[x][y][e] + lo[x][y][e]) +
+                         s.vec[64 + 16 * blk + 8 * y + c2 + (e & 1)] * (W[x][y][e] + lw[x][y][e]);
+            W[x][y][e] = lo[x][y][e] = 0.f;
+          }
+        if constexpr (KS > 1) put_frag<3>(ex.X[blk][0], from_acc<3>(U[x][0], U[x][1]), lane);
+      }
+      if constexpr (KS > 1) group_sync<KS>(group);
       // dX^T = dU^T T, then -beta gamma dX^T
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
+        if (KS > 1 && kk < ks) continue;
+        AFrag<3> fx;
+        if constexpr (KS > 1)
+          fx = get_frag<3>(ex.X[kk][0], lane);
+        else
+          fx = from_acc<3>(U[kk][0], U[kk][1]);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-          if (np <= kk) mma2(W[2 * np], W[2 * np + 1], fu, load_b_n<3>(s.Tm, kLdT, 16 * kk, 16 * np, lane));
+        for (int x = 0; x < NB; ++x) {
+          const int blk = KS > 1 ? ks : x;
+          if (KS > 1 || blk <= kk)
+            mma2(W[x][0], W[x][1], lo[x][0], lo[x][1], fx, load_tri_n<3>(s.Tm, kk, blk, lane));
+        }
       }
+      AFrag<3> fw[4];
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int x = 0; x < NB; ++x) {
+        const int blk = KS > 1 ? ks : x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 8 * n + c2 + (e & 1);
-          W[n][e] *= -s.vec[128 + t] * s.vec[t];
-        }
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 16 * blk + 8 * y + c2 + (e & 1);
+            W[x][y][e] = -s.vec[128 + t] * s.vec[t] * (W[x][y][e] + lo[x][y][e]);
+          }
+        fw[x] = from_acc<3>(W[x][0], W[x][1]);
+        if constexpr (KS > 1) put_frag<3>(ex.W[blk][0], fw[x], lane);
+      }
+      if constexpr (KS > 1) {
+        group_sync<KS>(group);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) fw[kk] = get_frag<3>(ex.W[kk][0], lane);
+      }
       const float full = s.vec[192];
+      AFrag<3> fd[4];
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n)
+      for (int kk = 0; kk < 4; ++kk) fd[kk] = load_a_m_scaled<3>(sd, ldv, 16 * kk, vs, lane, s.vec + 16 * kk, a.scale);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[n][e] *= full;
+      for (int np = 0; np < ND / 2; ++np) {
+        float hi[2][4] = {}, l2[2][4] = {};
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const AFrag<3> fx = from_acc<3>(W[2 * kk], W[2 * kk + 1]);
-        const AFrag<3> fd = load_a_m_scaled<3>(s.v, ldv, 16 * kk, 16 * warp, lane, s.vec + 16 * kk, a.scale);
-#pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          mma2(S[2 * np], S[2 * np + 1], fx, load_b_n<PI>(s.k, LD, 16 * kk, 16 * np, lane));
-          mma2(S[2 * np], S[2 * np + 1], fd, load_b_n<PI>(s.q, LD, 16 * kk, 16 * np, lane));
+        for (int kk = 0; kk < 4; ++kk) {
+          mma2(hi[0], hi[1], l2[0], l2[1], fw[kk], load_b_n<PI>(s.k, LD, 16 * kk, ks * (DK / KS) + 16 * np, lane));
+          mma2(hi[0], hi[1], l2[0], l2[1], fd[kk], load_b_n<PI>(s.q, LD, 16 * kk, ks * (DK / KS) + 16 * np, lane));
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[2 * np + y][e] = fmaf(full, S[2 * np + y][e], hi[y][e] + l2[y][e]);
       }
     }
-    __syncthreads();
-    if (NS == 1 && i > 0) fetch(i - 1);
+    if (a.stages == 1) {
+      __syncthreads();
+      if (i > 0) fetch(i - 1);
+    }
   }
-  if (a.dS0 && wg < nw) state_store<DK>(S, a.dS0 + bh * a.dk * a.dv, v0, a.dk, a.dv, lane);
+  if (a.dS0 && live) state_store<ND>(S, a.dS0 + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
+}
+
+constexpr int state_threads(int KS) { return KS == 4 ? 512 : 256; }  // at most
+
+template <typename T, int DK, int KS> __global__ void __launch_bounds__(state_threads(KS)) forward_kernel(const ChunkArgs a) {
+  state_pass<T, DK, KS, true, Dims<T, DK>::kOut>(a, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+// The two passes of the backward do not depend on each other: even blocks run the states forward,
+// odd ones their gradients backward.
+template <typename T, int DK, int KS> __global__ void __launch_bounds__(state_threads(KS)) both_kernel(const ChunkArgs a) {
+  if (blockIdx.x & 1)
+    bwd_state_pass<T, DK, KS>(a, blockIdx.x >> 1, blockIdx.y, blockIdx.z);
+  else
+    state_pass<T, DK, KS, false, 3>(a, blockIdx.x >> 1, blockIdx.y, blockIdx.z);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -583,8 +770,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
     const int h = hk * a.group + hi;
     const long long bh = (long long)b * a.H + h, at = bh * a.nc + i0, r0 = bh * a.L + t0;
     load_rows<T>(s.d, LDD, static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + t0 * a.os[2], a.os[2], n, a.dv, 128, a.vec_o, tid, 256);
-    load_tri(s.Tm, a.T + at * kTri, tid, 256);
-    load_tri(s.P, a.P + at * kTri, tid, 256);
+    load_tri_f32(s.Tm, a.T + at * 3 * kTri, tid, 256);
+    load_tri_f32(s.P, a.P + at * 3 * kTri, tid, 256);
     if (tid < kVec / 4) cp_async16(s.vec + 4 * tid, a.vec + at * kVec + 4 * tid, true);
     if (tid < kC / 2) cp_async16(s.G + 2 * tid, a.G + at * kC + 2 * tid, true);
     cp_async_commit();
