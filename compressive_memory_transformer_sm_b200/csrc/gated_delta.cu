@@ -196,7 +196,11 @@ template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
   rc = p.KS == 4 ? launch_chunk(both_kernel<T, DK, 4>, grid, p.threads, p.smem, kPhaseBwd, a, st)
                  : launch_chunk(both_kernel<T, DK, 1>, grid, p.threads, p.smem, kPhaseBwd, a, st);
   if (rc != INFINI_OK) return rc;
-  return launch_chunk(grad_kernel<T, DK>, dim3(a.nc, a.Hk, a.B), 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
+  const dim3 chunks(a.nc, a.Hk, a.B);
+  if constexpr (sizeof(T) == 2)
+    return launch_chunk(grad_bf16_kernel<DK>, chunks, 512, sizeof(GradSmemB<DK>), kPhaseBwd, a, st);
+  else
+    return launch_chunk(grad_kernel<T, DK>, chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
 }
 
 // Sequences of fewer tokens than this go token by token.
@@ -327,6 +331,9 @@ int backward(infini_attn_gated_delta_backward_params p) {
   a.vec_k = rows_vec(p.q, p.q_stride, p.dk, es) && rows_vec(p.k, p.k_stride, p.dk, es);
   a.vec_v = rows_vec(p.v, p.v_stride, p.dv, es);
   a.vec_o = rows_vec(p.d_out, p.d_out_stride, p.dv, es);
+  auto aligned = [](const void* x, int to) { return reinterpret_cast<uintptr_t>(x) % to == 0; };
+  a.vec_dq = p.dk % 2 == 0 && aligned(p.dq, 4) && aligned(p.dk_out, 4);
+  a.vec_dv = p.dv % 8 == 0 && aligned(p.dv_out, 16);
   a.nc = (int)n;
   space.place(a, w);
   const bool wide = padded_dk(p.dk) == 128;

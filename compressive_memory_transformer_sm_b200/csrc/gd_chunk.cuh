@@ -80,6 +80,7 @@ struct ChunkArgs {
   void* dvv;
   float* dg;
   float* dbeta;
+  bool vec_dq, vec_dv;  // pairs of dq and dk, 16-byte rows of dv can be written whole
   float* acc;  // grad, group > 1: [B Hk][nc][2][64][DK] running sums over the value heads of a key head
 };
 
@@ -107,6 +108,21 @@ template <int P> __device__ __forceinline__ BFrag<P> load_tri_n(const bf16* m, i
 #pragma unroll
   for (int p = 0; p < P; ++p) ldsm4t(b.r[p], x + p * kTri);
   return b;
+}
+// A[m][k] = m[m][k] of block (rb, cb), and A[m][k] = m[k][m].
+template <int P> __device__ __forceinline__ AFrag<P> load_tri_a_k(const bf16* m, int rb, int cb, int lane) {
+  AFrag<P> a;
+  const bf16* x = m + tri_block(rb, cb) * 256 + tri_at((lane & 8) + (lane & 7), (lane >> 4) * 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4(a.r[p], x + p * kTri);
+  return a;
+}
+template <int P> __device__ __forceinline__ AFrag<P> load_tri_a_m(const bf16* m, int rb, int cb, int lane) {
+  AFrag<P> a;
+  const bf16* x = m + tri_block(rb, cb) * 256 + tri_at((lane >> 4) * 8 + (lane & 7), lane & 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4t(a.r[p], x + p * kTri);
+  return a;
 }
 // A matrix of three parts as fp32 [64][kLdT].
 __device__ __forceinline__ void load_tri_f32(float* dst, const bf16* src, int tid, int nthr) {
@@ -1063,6 +1079,472 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
               if (x + 1 < a.dk) {
                 dq[o + 1] = in ? from_f32<T>(yq.y) : zero;
                 dkk[o + 1] = in ? from_f32<T>(yk.y) : zero;
+              }
+            }
+          }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ gradients, bf16
+// The same with 16 warps and every fp32 operand split once, where it is made: U and dX as three
+// planes [64][kLdG], T and P as they come, M + M^T and N as two.  Two warps share 16 value columns
+// (then 16 key columns): token blocks 0 and 3, or 1 and 2, so that the triangular products balance.
+constexpr int kLdG = 136, kPlaneG = kC * kLdG, kLdM = 72, kPlaneM = kC * kLdM;
+template <int DK> struct GradSmemB {
+  bf16 k[kC * (DK + 8)];
+  bf16 q[kC * (DK + 8)];
+  bf16 d[kPlaneG];      // d_out
+  bf16 U[3 * kPlaneG];
+  bf16 X[3 * kPlaneG];  // X, then dU, in fragments [strip][4][3][32] x 16 bytes; then dX
+  bf16 Tm[3 * kTri];
+  bf16 P[3 * kTri];     // P, then N in the first two planes
+  bf16 M[2 * kPlaneM];  // v [64][kLdG], then M + M^T
+  float vec[kVec];
+  double G[kC];
+  float tok[8][3][kC];
+  float rowP[10][16], colP[10][16], rowA[10][16], colA[10][16], rowB[10][16];
+  float sdot[8];
+};
+
+// Token sums of a warp's two blocks: x[block][tile][e] over the 16 value columns, to dst[64].
+__device__ __forceinline__ void sum_tokens(float (&x)[2][2][2], float* dst, int b0, int b1, int lane) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[i][t][e] += __shfl_xor_sync(0xffffffffu, x[i][t][e], o);
+  if (lane < 4)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        *reinterpret_cast<float2*>(dst + 16 * (i ? b1 : b0) + 8 * t + 2 * lane) = make_float2(x[i][t][0], x[i][t][1]);
+}
+
+template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const ChunkArgs a) {
+  constexpr int LD = DK + 8;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  GradSmemB<DK>& s = *reinterpret_cast<GradSmemB<DK>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int b = blockIdx.z, hk = blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int i0 = blockIdx.x;
+  const long long t0 = (long long)i0 * kC;
+  const int n = chunk_len(row_len(a, b), i0);
+  const int rows = chunk_len(a.L, i0);  // rows of the tensors in this chunk
+  bf16* dq = static_cast<bf16*>(a.dq) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
+  bf16* dkk = static_cast<bf16*>(a.dkk) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
+  const bf16 zero = from_f32<bf16>(0.f);
+  if (n == 0) {  // padding only
+    for (int x = tid; x < rows * a.dk; x += 512) dq[x] = dkk[x] = zero;
+    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
+      const long long r0 = ((long long)b * a.H + h) * a.L + t0;
+      for (int x = tid; x < rows * a.dv; x += 512) static_cast<bf16*>(a.dvv)[r0 * a.dv + x] = zero;
+      if (tid < rows) a.dg[r0 + tid] = a.dbeta[r0 + tid] = 0.f;
+    }
+    return;
+  }
+  const int strip = warp >> 1, half = warp & 1;
+  const int blks[2] = {half ? 1 : 0, half ? 2 : 3};
+  load_rows<bf16>(s.k, LD, static_cast<const bf16*>(a.k) + b * a.ks[0] + hk * a.ks[1] + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, 512);
+  load_rows<bf16>(s.q, LD, static_cast<const bf16*>(a.q) + b * a.qs[0] + hk * a.qs[1] + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, 512);
+  for (int hi = 0; hi < a.group; ++hi) {
+    const int h = hk * a.group + hi;
+    const long long bh = (long long)b * a.H + h, at = bh * a.nc + i0, r0 = bh * a.L + t0;
+    load_rows<bf16>(s.d, kLdG, static_cast<const bf16*>(a.d_out) + b * a.os[0] + h * a.os[1] + t0 * a.os[2], a.os[2], n, a.dv, 128, a.vec_o, tid, 512);
+    load_rows<bf16>(s.M, kLdG, static_cast<const bf16*>(a.v) + b * a.vs[0] + h * a.vs[1] + t0 * a.vs[2], a.vs[2], n, a.dv, 128, a.vec_v, tid, 512);
+    for (int i = tid; i < 3 * kTri / 8; i += 512) {
+      cp_async16(s.Tm + 8 * i, a.T + at * 3 * kTri + 8 * i, true);
+      cp_async16(s.P + 8 * i, a.P + at * 3 * kTri + 8 * i, true);
+    }
+    if (tid < kVec / 4) cp_async16(s.vec + 4 * tid, a.vec + at * kVec + 4 * tid, true);
+    if (tid < kC / 2) cp_async16(s.G + 2 * tid, a.G + at * kC + 2 * tid, true);
+    cp_async_commit();
+    const float4* snap = a.snap + at * nw * (DK / 8) * 32;
+    const float4* dsnap = a.dsnap + at * nw * (DK / 8) * 32;
+    cp_async_wait<0>();
+    __syncthreads();
+    float W[2][2][4] = {};
+    // ---- 1: U, dX and the sums over value columns; 16 value columns and two token blocks per warp
+    if (strip < nw) {
+      float R[2][2][4] = {}, Y[2][2][4] = {}, dot = 0.f;
+      const float4* ps = snap + strip * (DK / 8) * 32 + lane;
+      const float4* pd = dsnap + strip * (DK / 8) * 32 + lane;
+      float4 s0 = ps[0], s1 = ps[32], d0 = pd[0], d1 = pd[32];
+#pragma unroll 1
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        dot += s0.x * d0.x + s0.y * d0.y + s0.z * d0.z + s0.w * d0.w + s1.x * d1.x + s1.y * d1.y + s1.z * d1.z + s1.w * d1.w;
+        const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
+        const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
+        const AFrag<3> fs = from_acc<3>(sa, sb), fd = from_acc<3>(da, db);
+        if (kk + 1 < DK / 16) {
+          s0 = ps[(2 * kk + 2) * 32];
+          s1 = ps[(2 * kk + 3) * 32];
+          d0 = pd[(2 * kk + 2) * 32];
+          d1 = pd[(2 * kk + 3) * 32];
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const BFrag<1> bk = load_b_k<1>(s.k, LD, 16 * blks[x], 16 * kk, lane);
+          const BFrag<1> bq = load_b_k<1>(s.q, LD, 16 * blks[x], 16 * kk, lane);
+          mma2(R[x][0], R[x][1], fs, bk);
+          mma2(W[x][0], W[x][1], fd, bk);
+          mma2(Y[x][0], Y[x][1], fs, bq);
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) s.sdot[strip] = dot;
+      uint4* frag = reinterpret_cast<uint4*>(s.X) + strip * 4 * 3 * 32;
+      const int v0 = 16 * strip + g;
+      // sum_a = scale gamma dO.Y; then Y = V - gamma R (the error the write corrects), R stays K S
+      float sum_a[2][2][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float xa[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tk = 16 * blks[x] + 8 * t + c2 + e;
+            const float gam = s.vec[tk], be = s.vec[128 + tk];
+            sum_a[x][t][e] = a.scale * gam * (to_f32(s.d[tk * kLdG + v0]) * Y[x][t][e] + to_f32(s.d[tk * kLdG + v0 + 8]) * Y[x][t][2 + e]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              Y[x][t][2 * r + e] = to_f32(s.M[tk * kLdG + v0 + 8 * r]) - gam * R[x][t][2 * r + e];
+              xa[t][2 * r + e] = be * Y[x][t][2 * r + e];
+            }
+          }
+        put_frag<3>(frag + blks[x] * 96, from_acc<3>(xa[0], xa[1]), lane);
+      }
+      named_bar_sync(1 + strip, 64);
+      float U[2][2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk > blks[1]) break;
+        const AFrag<3> fx = get_frag<3>(frag + kk * 96, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (kk <= blks[x]) mma2(U[x][0], U[x][1], fx, load_tri_k<3>(s.Tm, blks[x], kk, lane));
+      }
+      float sum[2][2][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tk = 16 * blks[x] + 8 * t + c2 + e;
+            sum[x][t][e] = s.vec[64 + tk] * (W[x][t][e] * U[x][t][e] + W[x][t][2 + e] * U[x][t][2 + e]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float y = U[x][t][2 * r + e];
+#pragma unroll
+              for (int p = 0; p < 3; ++p) {
+                const bf16 w = from_f32<bf16>(y);
+                s.U[p * kPlaneG + tk * kLdG + v0 + 8 * r] = w;
+                y -= to_f32(w);
+              }
+              U[x][t][2 * r + e] = 0.f;
+            }
+          }
+      sum_tokens(sum, s.tok[strip][1], blks[0], blks[1], lane);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk < blks[0]) continue;
+        const AFrag<1> fd = load_a_m<1>(s.d, kLdG, 16 * kk, 16 * strip, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (kk >= blks[x]) mma2(U[x][0], U[x][1], fd, load_tri_n<3>(s.P, kk, blks[x], lane));
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            U[x][t][e] = a.scale * U[x][t][e] + s.vec[64 + 16 * blks[x] + 8 * t + c2 + (e & 1)] * W[x][t][e];
+            W[x][t][e] = 0.f;
+          }
+      named_bar_sync(1 + strip, 64);  // both warps have taken X
+#pragma unroll
+      for (int x = 0; x < 2; ++x) put_frag<3>(frag + blks[x] * 96, from_acc<3>(U[x][0], U[x][1]), lane);
+      named_bar_sync(1 + strip, 64);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk < blks[0]) continue;
+        const AFrag<3> fu = get_frag<3>(frag + kk * 96, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (kk >= blks[x]) mma2(W[x][0], W[x][1], fu, load_tri_n<3>(s.Tm, kk, blks[x], lane));
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tk = 16 * blks[x] + 8 * t + c2 + e;
+            sum_a[x][t][e] -= s.vec[128 + tk] * s.vec[tk] * (W[x][t][e] * R[x][t][e] + W[x][t][2 + e] * R[x][t][2 + e]);
+            sum[x][t][e] = W[x][t][e] * Y[x][t][e] + W[x][t][2 + e] * Y[x][t][2 + e];
+          }
+      sum_tokens(sum_a, s.tok[strip][0], blks[0], blks[1], lane);
+      sum_tokens(sum, s.tok[strip][2], blks[0], blks[1], lane);
+    }
+    __syncthreads();  // every fragment has been read: dX takes their place
+    if (strip < nw)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = 16 * blks[x] + 8 * t + c2 + (e & 1);
+            float y = W[x][t][e];
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+              const bf16 w = from_f32<bf16>(y);
+              s.X[p * kPlaneG + tk * kLdG + 16 * strip + g + 8 * (e >> 1)] = w;
+              y -= to_f32(w);
+            }
+          }
+    __syncthreads();
+    // ---- 2: a 16 x 16 block of dA in each of warps 0-9, one or two of dP in the others; dV
+    {
+      bf16* dv = static_cast<bf16*>(a.dvv) + r0 * a.dv;
+      for (int x = tid; x < kC * 16; x += 512) {
+        const int t = x >> 4, y = (x & 15) * 8;
+        if (t >= rows || y >= a.dv) continue;
+        const float be = s.vec[128 + t];
+        const uint4 u0 = *reinterpret_cast<const uint4*>(s.X + t * kLdG + y);
+        const uint4 u1 = *reinterpret_cast<const uint4*>(s.X + kPlaneG + t * kLdG + y);
+        const uint32_t p0[4] = {u0.x, u0.y, u0.z, u0.w}, p1[4] = {u1.x, u1.y, u1.z, u1.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = t < n ? pack_bf16x2(be * (bf16_lo(p0[i]) + bf16_lo(p1[i])), be * (bf16_hi(p0[i]) + bf16_hi(p1[i]))) : 0u;
+        if (a.dv % 8 == 0 && a.vec_dv) {
+          *reinterpret_cast<uint4*>(dv + (long long)t * a.dv + y) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          const bf16* w = reinterpret_cast<const bf16*>(o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (y + i < a.dv) dv[(long long)t * a.dv + y + i] = w[i];
+        }
+      }
+      const bool is_a = warp < 10;
+      for (int blk = is_a ? warp : warp - 10; blk < 10; blk += is_a ? 10 : 6) {
+        const int rb = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, cb = blk - rb * (rb + 1) / 2;
+        float acc[2][4] = {}, lo[2][4] = {}, kk2[2][4] = {};
+#pragma unroll 1
+        for (int kk = 0; kk < nw; ++kk) {
+          const BFrag<3> fu = load_b_k<3>(s.U, kPlaneG, kLdG, 16 * cb, 16 * kk, lane);
+          if (is_a)
+            mma2(acc[0], acc[1], lo[0], lo[1], load_a_k<3>(s.X, kPlaneG, kLdG, 16 * rb, 16 * kk, lane), fu);
+          else
+            mma2(acc[0], acc[1], lo[0], lo[1], load_a_k<1>(s.d, kLdG, 16 * rb, 16 * kk, lane), fu);
+        }
+        if (is_a)
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma2(kk2[0], kk2[1], load_a_k<1>(s.k, LD, 16 * rb, 16 * kk, lane), load_b_k<1>(s.k, LD, 16 * cb, 16 * kk, lane));
+        float row[2] = {}, rowb[2] = {};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float col[2] = {};
+          const int jl = 8 * t + c2, j = 16 * cb + jl;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int il = g + 8 * r, i = 16 * rb + il;
+            float m[2], dec[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              m[e] = acc[t][2 * r + e] + lo[t][2 * r + e];
+              dec[e] = (is_a ? i > j + e : i >= j + e) ? expf((float)(s.G[i] - s.G[j + e])) : 0.f;
+            }
+            if (is_a) {
+              const float be = s.vec[128 + i];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float ab = -m[e] * dec[e] * kk2[t][2 * r + e];
+                rowb[r] += ab;
+                row[r] += be * ab;
+                col[e] += be * ab;
+                m[e] *= -be * dec[e];
+              }
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t w = pack_bf16x2(m[0], m[1]);
+                bf16* M = s.M + p * kPlaneM;
+                // the pair lies on one side of the diagonal or across it
+                if (i > j + 1) *reinterpret_cast<uint32_t*>(M + i * kLdM + j) = w;
+                else if (i >= j) M[i * kLdM + j] = from_f32<bf16>(m[0]);
+                if (i == j + 1) M[i * kLdM + j + 1] = zero;
+                if (i > j) M[j * kLdM + i] = __ushort_as_bfloat16((unsigned short)(w & 0xffffu));
+                if (i > j + 1) M[(j + 1) * kLdM + i] = __ushort_as_bfloat16((unsigned short)(w >> 16));
+                m[0] -= bf16_lo(w);
+                m[1] -= bf16_hi(w);
+              }
+            } else {
+              bf16* P = s.P + blk * 256 + tri_at(il, jl);
+              const uint32_t p0 = *reinterpret_cast<const uint32_t*>(P), p1 = *reinterpret_cast<const uint32_t*>(P + kTri),
+                             p2 = *reinterpret_cast<const uint32_t*>(P + 2 * kTri);
+              const float pe[2] = {(bf16_lo(p2) + bf16_lo(p1)) + bf16_lo(p0), (bf16_hi(p2) + bf16_hi(p1)) + bf16_hi(p0)};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float dp = a.scale * m[e], y = dec[e] != 0.f ? dp * pe[e] : 0.f;
+                row[r] += y;
+                col[e] += y;
+                m[e] = dp * dec[e];
+              }
+              put_parts<2>(P, kTri, m[0], m[1]);
+            }
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            col[0] += __shfl_xor_sync(0xffffffffu, col[0], o);
+            col[1] += __shfl_xor_sync(0xffffffffu, col[1], o);
+          }
+          if (lane < 4) {
+            (is_a ? s.colA : s.colP)[blk][jl] = col[0];
+            (is_a ? s.colA : s.colP)[blk][jl + 1] = col[1];
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            row[r] += __shfl_xor_sync(0xffffffffu, row[r], o);
+            rowb[r] += __shfl_xor_sync(0xffffffffu, rowb[r], o);
+          }
+        if ((lane & 3) == 0)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            (is_a ? s.rowA : s.rowP)[blk][g + 8 * r] = row[r];
+            if (is_a) s.rowB[blk][g + 8 * r] = rowb[r];
+          }
+      }
+    }
+    __syncthreads();
+    // ---- 3: dg, dbeta (warp 0, two tokens a lane); dQ and dK, 16 key columns and 32 tokens per warp
+    if (warp == 15) {
+      double x[2];
+      double sum_e = 0.;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i, tb = t >> 4, tl = t & 15;
+        float av = 0.f, ev = 0.f, bv = 0.f, pos = 0.f, neg = 0.f;
+        for (int w = 0; w < nw; ++w) {
+          av += s.tok[w][0][t];
+          ev += s.tok[w][1][t];
+          bv += s.tok[w][2][t];
+        }
+        for (int c = 0; c <= tb; ++c) {
+          pos += s.rowP[tri_block(tb, c)][tl] + s.rowA[tri_block(tb, c)][tl];
+          bv += s.rowB[tri_block(tb, c)][tl];
+        }
+        for (int r = tb; r < 4; ++r) neg += s.colP[tri_block(r, tb)][tl] + s.colA[tri_block(r, tb)][tl];
+        x[i] = (double)av - ev + pos - neg;
+        sum_e += ev;
+        if (t < rows) a.dbeta[r0 + t] = t < n ? bv : 0.f;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) sum_e += __shfl_xor_sync(0xffffffffu, sum_e, o);
+      float dot = 0.f;
+      for (int w = 0; w < nw; ++w) dot += s.sdot[w];
+      if (lane == 31) x[1] += sum_e + (double)s.vec[192] * dot;
+      double sum = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += y;
+      }
+      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)sum : 0.f;
+      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum - x[0]) : 0.f;
+    }
+    if (strip < DK / 16) {
+      const int n0 = 16 * strip;
+      float Q[2][2][4] = {}, K[2][2][4] = {}, V[2][2][4] = {};
+      const float4* ps = snap + 2 * strip * 32 + lane;
+      const float4* pd = dsnap + 2 * strip * 32 + lane;
+#pragma unroll 2
+      for (int kw = 0; kw < nw; ++kw) {
+        const BFrag<2> fs = b_from_acc<2>(ps[kw * (DK / 8) * 32], ps[kw * (DK / 8) * 32 + 32]);
+        const BFrag<2> fd = b_from_acc<2>(pd[kw * (DK / 8) * 32], pd[kw * (DK / 8) * 32 + 32]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int m0 = 32 * half + 16 * x;
+          mma2(Q[x][0], Q[x][1], load_a_k<1>(s.d, kLdG, m0, 16 * kw, lane), fs);
+          mma2(K[x][0], K[x][1], load_a_k<2>(s.X, kPlaneG, kLdG, m0, 16 * kw, lane), fs);
+          mma2(V[x][0], V[x][1], load_a_k<2>(s.U, kPlaneG, kLdG, m0, 16 * kw, lane), fd);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tk = 32 * half + 16 * x + g + 8 * r;
+          const float gam = s.vec[tk], be = s.vec[128 + tk], rho = s.vec[64 + tk];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 2 * r; e < 2 * r + 2; ++e) {
+              Q[x][t][e] *= a.scale * gam;
+              K[x][t][e] = rho * V[x][t][e] - be * gam * K[x][t][e];
+            }
+        }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const BFrag<1> bk = load_b_n<1>(s.k, LD, 16 * kk, n0, lane), bq = load_b_n<1>(s.q, LD, 16 * kk, n0, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int mt = 2 * half + x;
+          if (kk <= mt) mma2(Q[x][0], Q[x][1], load_tri_a_k<2>(s.P, mt, kk, lane), bk);
+          mma2(K[x][0], K[x][1], load_a_k<2>(s.M, kPlaneM, kLdM, 16 * mt, 16 * kk, lane), bk);
+          if (kk >= mt) mma2(K[x][0], K[x][1], load_tri_a_m<2>(s.P, kk, mt, lane), bq);
+        }
+      }
+      float* acc = a.acc + (((long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int tk = 32 * half + 16 * x + g + 8 * r, col = n0 + 8 * t + c2;
+            float2 yq = make_float2(Q[x][t][2 * r], Q[x][t][2 * r + 1]), yk = make_float2(K[x][t][2 * r], K[x][t][2 * r + 1]);
+            if (a.group > 1) {  // the same thread holds this element for every value head of the key head
+              float2* pq = reinterpret_cast<float2*>(acc + tk * DK + col);
+              float2* pk = reinterpret_cast<float2*>(acc + (kC + tk) * DK + col);
+              if (hi > 0) {
+                const float2 oq = *pq, ok = *pk;
+                yq.x += oq.x; yq.y += oq.y; yk.x += ok.x; yk.y += ok.y;
+              }
+              if (hi + 1 < a.group) {
+                *pq = yq;
+                *pk = yk;
+                continue;
+              }
+            }
+            if (tk < rows) {
+              const long long o = (long long)tk * a.dk + col;
+              if (tk >= n) yq = yk = make_float2(0.f, 0.f);
+              if (a.vec_dq && col < a.dk) {
+                *reinterpret_cast<uint32_t*>(dq + o) = pack_bf16x2(yq.x, yq.y);
+                *reinterpret_cast<uint32_t*>(dkk + o) = pack_bf16x2(yk.x, yk.y);
+              } else {
+                if (col < a.dk) {
+                  dq[o] = from_f32<bf16>(yq.x);
+                  dkk[o] = from_f32<bf16>(yk.x);
+                }
+                if (col + 1 < a.dk) {
+                  dq[o + 1] = from_f32<bf16>(yq.y);
+                  dkk[o + 1] = from_f32<bf16>(yk.y);
+                }
               }
             }
           }

@@ -230,6 +230,24 @@ template <int P> __device__ __forceinline__ AFrag<P> load_a_m(const bf16* m, int
   for (int p = 0; p < P; ++p) ldsm4t(a.r[p], x + p * plane);
   return a;
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 block of 16-bit elements
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// B[k][n] = x[k][n] from the accumulator tiles of x: rows k = 16, columns the tiles' 2 x 8.
+template <int P> __device__ __forceinline__ BFrag<P> b_from_acc(const float4& t0, const float4& t1) {
+  BFrag<P> b;
+  split<P>(t0.x, t0.y, b.r, 0);
+  split<P>(t0.z, t0.w, b.r, 1);
+  split<P>(t1.x, t1.y, b.r, 2);
+  split<P>(t1.z, t1.w, b.r, 3);
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b.r[p][i] = transpose8(b.r[p][i]);
+  return b;
+}
 // A fragments to and from shared memory as they are: [part][lane], 16 bytes each
 template <int P> __device__ __forceinline__ void put_frag(uint4* dst, const AFrag<P>& a, int lane) {
 #pragma unroll
