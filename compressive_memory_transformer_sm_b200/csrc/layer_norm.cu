@@ -25,33 +25,29 @@ namespace ln {
 constexpr int kMaxD = 16384;
 
 template <int VEC> struct Floats { float v[VEC]; };
+// VEC consecutive elements as they lie in memory (16-byte aligned when VEC > 1).
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<__nv_bfloat16, 8> { uint4 u; };
+template <> struct Raw<float, 4> { float4 u; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 u; };
+template <> struct Raw<float, 1> { float u; };
 
-// VEC consecutive elements at p (16-byte aligned when VEC > 1).
-template <int VEC> __device__ __forceinline__ Floats<VEC> load_vec(const __nv_bfloat16* p) {
+template <int VEC, typename T> __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
+  return *reinterpret_cast<const Raw<T, VEC>*>(p);
+}
+template <typename T, int VEC> __device__ __forceinline__ Floats<VEC> floats(const Raw<T, VEC>& r) {
   Floats<VEC> f;
   if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f.v[2 * i] = bf16_lo(w[i]);
       f.v[2 * i + 1] = bf16_hi(w[i]);
     }
-  } else {
-    f.v[0] = __bfloat162float(*p);
-  }
-  return f;
-}
-template <int VEC> __device__ __forceinline__ Floats<VEC> load_vec(const float* p) {
-  Floats<VEC> f;
-  if constexpr (VEC == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   } else if constexpr (VEC == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    f = {{a.x, a.y, a.z, a.w}};
+    f = {{r.u.x, r.u.y, r.u.z, r.u.w}};
   } else {
-    f.v[0] = *p;
+    f.v[0] = to_f32(r.u);
   }
   return f;
 }
@@ -74,19 +70,30 @@ template <int VEC> __device__ __forceinline__ void store_vec(float* p, const Flo
     *p = f.v[0];
   }
 }
-// weight / bias elements, bf16 or fp32 (scalar loads where the vector would not be aligned: a
-// 4-element vector of bf16 weights beside fp32 rows)
+// weight / bias elements, bf16 or fp32
 template <int VEC> __device__ __forceinline__ Floats<VEC> load_weight(const void* p, bool f32, long long at) {
-  if (f32) return load_vec<VEC>(static_cast<const float*>(p) + at);
-  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p) + at;
-  if constexpr (VEC == 8) {
-    return load_vec<8>(w);
-  } else {
-    Floats<VEC> f;
+  Floats<VEC> f;
+  if (f32) {
+    const float* w = static_cast<const float*>(p) + at;
+    if constexpr (VEC == 8) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f.v[e] = __bfloat162float(w[e]);
-    return f;
+      for (int i = 0; i < 2; ++i) {
+        const Floats<4> h = floats(load_raw<4>(w + 4 * i));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[4 * i + e] = h.v[e];
+      }
+    } else {
+      f = floats(load_raw<VEC>(w));
+    }
+  } else {
+    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p) + at;
+    if constexpr (VEC == 8)
+      f = floats(load_raw<8>(w));
+    else
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f.v[e] = to_f32(w[e]);
   }
+  return f;
 }
 
 // Sums of N values over the TPR threads of a row, the same in all of them.  Above a warp the
@@ -128,18 +135,39 @@ struct Args {
   bool has_bias;  // backward: dbias is wanted
 };
 
-template <int TPR> constexpr int kBlockThreads = TPR < 256 ? 256 : TPR;
+// Threads per block: rows of at most a warp share a block of 128, wider rows have a block each.
+template <int TPR> constexpr int kBlockThreads = TPR < 128 ? 128 : TPR;
+// Elements per thread up to which the weights stay in registers for all the rows of a block.
+// (Re-read for each row they cost four times the row itself from L2: 146 us at 32768 x 4096 bf16.)
+constexpr int kKeep = 16;
 
-// xs: the row's elements less their mean; returns rstd.
+// A thread's part of row `row`; zeros behind the row's end.
 template <typename T, int VEC, int TPR, int NV>
-__device__ __forceinline__ float centre(const T* x, bool active, int lane, int D, float (&xs)[NV][VEC], float* red,
-                                        int sub, int red_stride) {
-  float s[1] = {0.f};
+__device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* x, long long row, bool active, int lane, int D) {
+  const T* p = static_cast<const T*>(x) + row * D;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int at = (v * TPR + lane) * VEC;
-    Floats<VEC> f = {};
-    if (active && at < D) f = load_vec<VEC>(x + at);
+    r[v] = Raw<T, VEC>{};
+    if (active && at < D) r[v] = load_raw<VEC>(p + at);
+  }
+}
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_weights(Floats<VEC> (&w)[NV], const void* p, bool f32, int lane, int D) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (v * TPR + lane) * VEC;
+    w[v] = {};
+    if (p && at < D) w[v] = load_weight<VEC>(p, f32, at);
+  }
+}
+// xs: the row's elements less their mean, 0 behind its end; returns the variance.
+template <typename T, int VEC, int TPR, int NV>
+__device__ __forceinline__ float centre(const Raw<T, VEC> (&r)[NV], int lane, int D, float (&xs)[NV][VEC], float* red, int sub, int red_stride) {
+  float s[1] = {0.f};
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const Floats<VEC> f = floats(r[v]);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       xs[v][e] = f.v[e];
@@ -165,26 +193,42 @@ __device__ __forceinline__ float centre(const T* x, bool active, int lane, int D
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_forward_kernel(const Args a) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR, NW = TPR > 32 ? TPR / 32 : 1;
+  constexpr bool KEEP = NV * VEC <= kKeep;
   __shared__ float red[2 * RPB * NW];
   const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
-  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
-    const long long row = base + sub;
+  const long long step = (long long)gridDim.x * RPB;
+  long long row = (long long)blockIdx.x * RPB + sub;
+  Raw<T, VEC> next[NV];
+  load_row<T, VEC, TPR, NV>(next, a.x, row, row < a.rows, lane, a.D);
+  Floats<VEC> w[KEEP ? NV : 1], b[KEEP ? NV : 1];
+  if constexpr (KEEP) {
+    load_weights<VEC, TPR, NV>(w, a.weight, a.w32, lane, a.D);
+    load_weights<VEC, TPR, NV>(b, a.bias, a.w32, lane, a.D);
+  }
+  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
+    Raw<T, VEC> cur[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) cur[v] = next[v];
+    load_row<T, VEC, TPR, NV>(next, a.x, row + step, row + step < a.rows, lane, a.D);
     float xs[NV][VEC];
-    const float var = centre<T, VEC, TPR, NV>(static_cast<const T*>(a.x) + row * a.D, active, lane, a.D, xs, red, sub,
-                                              RPB * NW);
+    const float var = centre<T, VEC, TPR, NV>(cur, lane, a.D, xs, red, sub, RPB * NW);
     const float rstd = 1.f / sqrtf(var + a.eps);
     if (!active) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int at = (v * TPR + lane) * VEC;
       if (at < a.D) {
-        const Floats<VEC> w = load_weight<VEC>(a.weight, a.w32, at);
-        Floats<VEC> b = {};
-        if (a.bias) b = load_weight<VEC>(a.bias, a.w32, at);
-        Floats<VEC> o;
+        Floats<VEC> wv, bv = {}, o;
+        if constexpr (KEEP) {
+          wv = w[v];
+          bv = b[v];
+        } else {
+          wv = load_weight<VEC>(a.weight, a.w32, at);
+          if (a.bias) bv = load_weight<VEC>(a.bias, a.w32, at);
+        }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o.v[e] = fmaf(xs[v][e] * rstd, w.v[e], b.v[e]);
+        for (int e = 0; e < VEC; ++e) o.v[e] = fmaf(xs[v][e] * rstd, wv.v[e], bv.v[e]);
         store_vec<VEC>(static_cast<T*>(a.y) + row * a.D + at, o);
       }
     }
@@ -194,35 +238,50 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_forward_kernel(const Ar
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const Args a) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR, NW = TPR > 32 ? TPR / 32 : 1, E = NV * VEC;
+  constexpr bool KEEP = E <= kKeep;
   // statistics of the two sums of a row, then (RPB > 1) the rows' accumulators of the block
   __shared__ float red[4 * RPB * NW];
   extern __shared__ float acc[];  // [RPB > 1 ? TPR * E * 2 : 0]
   const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
+  const long long step = (long long)gridDim.x * RPB;
+  long long row = (long long)blockIdx.x * RPB + sub;
+  Raw<T, VEC> nx[NV], nd[NV];
+  load_row<T, VEC, TPR, NV>(nx, a.x, row, row < a.rows, lane, a.D);
+  load_row<T, VEC, TPR, NV>(nd, a.dy, row, row < a.rows, lane, a.D);
+  Floats<VEC> w[KEEP ? NV : 1];
+  if constexpr (KEEP) load_weights<VEC, TPR, NV>(w, a.weight, a.w32, lane, a.D);
   float dw[NV][VEC] = {}, db[NV][VEC] = {};
-  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
-    const long long row = base + sub;
+  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
+    Raw<T, VEC> cx[NV], cd[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      cx[v] = nx[v];
+      cd[v] = nd[v];
+    }
+    load_row<T, VEC, TPR, NV>(nx, a.x, row + step, row + step < a.rows, lane, a.D);
+    load_row<T, VEC, TPR, NV>(nd, a.dy, row + step, row + step < a.rows, lane, a.D);
     float xs[NV][VEC];
-    const float var = centre<T, VEC, TPR, NV>(static_cast<const T*>(a.x) + row * a.D, active, lane, a.D, xs, red, sub,
-                                              RPB * NW);
+    const float var = centre<T, VEC, TPR, NV>(cx, lane, a.D, xs, red, sub, RPB * NW);
     const float rstd = 1.f / sqrtf(var + a.eps);
-    float h[NV][VEC], s[2] = {0.f, 0.f};
+    float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int at = (v * TPR + lane) * VEC;
-      Floats<VEC> d = {}, w = {};
-      if (active && at < a.D) {
-        d = load_vec<VEC>(static_cast<const T*>(a.dy) + row * a.D + at);
-        w = load_weight<VEC>(a.weight, a.w32, at);
-      }
+      const Floats<VEC> d = floats(cd[v]);
+      Floats<VEC> wv = {};
+      if constexpr (KEEP)
+        wv = w[v];
+      else if (at < a.D)
+        wv = load_weight<VEC>(a.weight, a.w32, at);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         xs[v][e] *= rstd;
         dw[v][e] = fmaf(d.v[e], xs[v][e], dw[v][e]);
         db[v][e] += d.v[e];
-        h[v][e] = d.v[e] * w.v[e];
-        s[0] += h[v][e];
-        s[1] = fmaf(h[v][e], xs[v][e], s[1]);
+        const float h = d.v[e] * wv.v[e];
+        s[0] += h;
+        s[1] = fmaf(h, xs[v][e], s[1]);
       }
     }
     row_sum<TPR>(s, red + 2 * RPB * NW, sub);
@@ -232,9 +291,14 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const A
       for (int v = 0; v < NV; ++v) {
         const int at = (v * TPR + lane) * VEC;
         if (at < a.D) {
-          Floats<VEC> o;
+          const Floats<VEC> d = floats(cd[v]);
+          Floats<VEC> wv, o;
+          if constexpr (KEEP)
+            wv = w[v];
+          else
+            wv = load_weight<VEC>(a.weight, a.w32, at);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) o.v[e] = rstd * (h[v][e] - m0 - xs[v][e] * m1);
+          for (int e = 0; e < VEC; ++e) o.v[e] = rstd * (d.v[e] * wv.v[e] - m0 - xs[v][e] * m1);
           store_vec<VEC>(static_cast<T*>(a.y) + row * a.D + at, o);
         }
       }
@@ -278,44 +342,54 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const A
   }
 }
 
-// dweight, dbias: the sum of the blocks' partials, in their order (32 columns per block; eight
-// interleaved ranges of blocks, then those eight sums).
-__global__ void __launch_bounds__(256) ln_reduce_kernel(const float* partial, int parts, int D, void* dw, void* db,
-                                                        bool w32) {
-  __shared__ float s[8][33];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
+// dweight, dbias: the sum of the blocks' partials, in their order (32 columns per block; 32
+// interleaved ranges of blocks, then those 32 sums).
+__global__ void __launch_bounds__(1024) ln_reduce_kernel(const float* partial, int parts, int D, void* dw, void* db, bool w32) {
+  __shared__ float s[32][33];
+  const int x = threadIdx.x % 32, col = blockIdx.x * 32 + x, r = threadIdx.x / 32;
   const bool is_b = blockIdx.y == 1;
-  float x = 0.f;
+  float y = 0.f;
   if (col < D)
-    for (int p = r; p < parts; p += 8) x += partial[((long long)p * 2 + is_b) * D + col];
-  s[r][threadIdx.x % 32] = x;
+#pragma unroll 4
+    for (int p = r; p < parts; p += 32) y += partial[((long long)p * 2 + is_b) * D + col];
+  s[r][x] = y;
   __syncthreads();
-  if (r == 0 && col < D) {
-    float t = 0.f;
+  // warp r sums column r
+  float t = s[x][r];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x];
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int c = blockIdx.x * 32 + r;
+  if (x == 0 && c < D) {
     void* out = is_b ? db : dw;
     if (w32)
-      static_cast<float*>(out)[col] = t;
+      static_cast<float*>(out)[c] = t;
     else
-      static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(t);
+      static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(t);
   }
 }
 
-// Blocks of the backward's row loop: four per SM at most, so that the partials stay few.
+// Blocks of the row loops.  Forward: as many as are resident (one per row at most).  Backward: every
+// block leaves a partial of 2 D sums, so no more than keep them small beside the rows.
 int backward_blocks(long long rows, int rpb) {
   return (int)std::min<long long>((rows + rpb - 1) / rpb, 4LL * kSms);
 }
 
+template <typename F> int resident_blocks(F* kernel, int threads, size_t smem) {
+  int n = 0;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) == cudaSuccess && n > 0 ? n * kSms : kSms;
+}
+
 template <typename T, int VEC, int TPR, int NV> int launch(const Args& a, bool bwd, cudaStream_t st, int* parts) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR;
+  const long long most = (a.rows + RPB - 1) / RPB;
   if (!bwd) {
-    const int grid = (int)std::min<long long>((a.rows + RPB - 1) / RPB, 1LL << 30);
+    static const int resident = resident_blocks(ln_forward_kernel<T, VEC, TPR, NV>, TH, 0);
     LaunchScope scope(kPhasePre, st);
-    ln_forward_kernel<T, VEC, TPR, NV><<<grid, TH, 0, st>>>(a);
+    ln_forward_kernel<T, VEC, TPR, NV><<<(int)std::min<long long>(most, resident), TH, 0, st>>>(a);
   } else {
-    *parts = backward_blocks(a.rows, RPB);
     const size_t smem = RPB > 1 ? (size_t)TPR * NV * VEC * 2 * 4 : 0;
+    static const int resident = resident_blocks(ln_backward_kernel<T, VEC, TPR, NV>, TH, smem);
+    *parts = (int)std::min<long long>(backward_blocks(a.rows, RPB), resident);
     LaunchScope scope(kPhaseBwd, st);
     ln_backward_kernel<T, VEC, TPR, NV><<<*parts, TH, smem, st>>>(a);
   }
@@ -332,7 +406,7 @@ template <typename T> int dispatch(const Args& a, bool vec, bool bwd, cudaStream
     if (n <= 16) return launch<T, V, 16, 1>(a, bwd, st, parts);
     if (n <= 32) return launch<T, V, 32, 1>(a, bwd, st, parts);
     if (n <= 64) return launch<T, V, 32, 2>(a, bwd, st, parts);
-    if (n <= 128) return launch<T, V, 128, 1>(a, bwd, st, parts);
+    if (n <= 128) return launch<T, V, 32, 4>(a, bwd, st, parts);
     if (n <= 256) return launch<T, V, 128, 2>(a, bwd, st, parts);
     if (n <= 512) return launch<T, V, 256, 2>(a, bwd, st, parts);
     if (n <= 1024) return launch<T, V, 512, 2>(a, bwd, st, parts);
@@ -436,7 +510,7 @@ int infini_attn_layer_norm_backward(const void* x, const void* weight, const voi
                            : ln::dispatch<__nv_bfloat16>(a, vec, true, stream, &parts);
   if (rc == INFINI_OK) {
     LaunchScope scope(kPhaseBwd, stream);
-    ln::ln_reduce_kernel<<<dim3((D + 31) / 32, dbias ? 2 : 1), 256, 0, stream>>>(a.partial, parts, D, dweight, dbias, a.w32);
+    ln::ln_reduce_kernel<<<dim3((D + 31) / 32, dbias ? 2 : 1), 1024, 0, stream>>>(a.partial, parts, D, dweight, dbias, a.w32);
     rc = launch_status();
   }
   if (!workspace && cudaFreeAsync(w, stream) != cudaSuccess && rc == INFINI_OK) rc = INFINI_ERR_WORKSPACE;
