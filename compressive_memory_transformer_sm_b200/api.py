@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -173,15 +174,21 @@ class GatedDeltaBackwardParams(ctypes.Structure):
     ]
 
 
-lib.infini_attn_gated_delta_backward.argtypes = [ctypes.POINTER(GatedDeltaBackwardParams)]
+# The same structs packed from a flat list of fields: a tenth of the time of filling a ctypes structure, which is
+# what a call for one token costs most.
+_GD_FORWARD = struct.Struct("@8P3iq3if18qPNP")
+_GD_STEP = struct.Struct("@8P3iq3if12qP")
+_GD_BACKWARD = struct.Struct("@15P3iq3if18qPNP")
+
+lib.infini_attn_gated_delta_backward.argtypes = [_vp]
 lib.infini_attn_gated_delta_backward.restype = _i
 lib.infini_attn_gated_delta_backward_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaBackwardParams)]
 lib.infini_attn_gated_delta_backward_workspace_size.restype = ctypes.c_size_t
-lib.infini_attn_gated_delta_forward.argtypes = [ctypes.POINTER(GatedDeltaParams)]
+lib.infini_attn_gated_delta_forward.argtypes = [_vp]
 lib.infini_attn_gated_delta_forward.restype = _i
 lib.infini_attn_gated_delta_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaParams)]
 lib.infini_attn_gated_delta_workspace_size.restype = ctypes.c_size_t
-lib.infini_attn_gated_delta_step.argtypes = [ctypes.POINTER(GatedDeltaStepParams)]
+lib.infini_attn_gated_delta_step.argtypes = [_vp]
 lib.infini_attn_gated_delta_step.restype = _i
 lib.infini_attn_gated_delta_params_size.argtypes = [_i]
 lib.infini_attn_gated_delta_params_size.restype = ctypes.c_size_t
@@ -230,7 +237,7 @@ def _stream(stream):
 def _on(stream):
     """Makes ``stream`` torch's current stream, so that the tensors a call returns belong to it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -452,36 +459,46 @@ def infini_attn_backward_workspace_size(B, H, L, N, dk, dv, mode=LINEAR, flags: 
     return int(lib.infini_attn_backward_workspace_size(ctypes.byref(p)))
 
 
-def _tensors(where: str, shapes: dict):
-    """Marshalling checks of the gated delta rule and the layer norm: name -> (tensor, shape, dtype); every tensor
-    with this shape and type, its last dimension contiguous, on one CUDA device.  Returns that device."""
-    dev = None
-    for name, (t, shape, dtype) in shapes.items():
+def _tensors(where: str, table):
+    """Marshalling checks of the gated delta rule and the layer norm: (name, tensor, shape, dtype, layout) rows; every
+    tensor with this shape and type on one CUDA device, laid out "c" contiguous, "r" with its last dimension
+    contiguous, "s" with any strides.  Returns the device's index."""
+    for name, t, shape, dtype, layout in table:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch.Tensor")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.dtype != dtype:
             raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-    for name, (t, _, _) in shapes.items():
-        if not t.is_cuda:
-            raise ValueError(f"{where}: {name} must be on a CUDA device, got {t.device}")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, the tensors before it on {dev}")
-        dev = t.device
+        if layout == "c":
+            if not t.is_contiguous():
+                raise ValueError(f"{where}: {name} must be contiguous")
+        else:
+            stride = t.stride()
+            if layout == "r":
+                if stride[-1] != 1 and shape[-1] > 1:
+                    raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
+                stride = stride[:-1]
+            if not any(stride) and t.numel() > shape[-1]:
+                raise ValueError(f"{where}: {name} must not be broadcast along every dimension")
+    dev = table[0][1].get_device()
+    for name, t, _, _, _ in table:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{where}: {name} must be on the CUDA device of the others, got {t.device}")
     return dev
 
 
-def _contiguous(where: str, **tensors):
-    for name, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
+def _device(index: int):
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _rows_contiguous(where: str, **tensors):
-    for name, t in tensors.items():
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
+def _stream_on(stream, index: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream(stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _elem(where: str, t):
@@ -492,12 +509,17 @@ def _elem(where: str, t):
     return t.dtype
 
 
-def _workspace(where: str, p, workspace):
-    if workspace is not None:
-        if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
-            raise ValueError(f"{where}: workspace must be a contiguous device tensor")
-        p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.numel() * workspace.element_size()
+def _space(where: str, workspace, dev: int):
+    """(pointer, bytes) of a caller's workspace."""
+    if workspace is None:
+        return 0, 0
+    if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
+        raise ValueError(f"{where}: workspace must be a contiguous tensor on the others' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _gated_delta_shapes(where, q, k, v, g, beta, lens):
@@ -507,11 +529,11 @@ def _gated_delta_shapes(where, q, k, v, g, beta, lens):
         raise ValueError(f"{where}: q and v must have 4 dimensions")
     B, Hk, L, dk = q.shape
     H, dv = v.shape[1], v.shape[3]
-    f32 = torch.float32
-    table = dict(q=(q, (B, Hk, L, dk), t), k=(k, (B, Hk, L, dk), t), v=(v, (B, H, L, dv), t), g=(g, (B, H, L), f32),
-                 beta=(beta, (B, H, L), f32))
+    keys, heads = (B, Hk, L, dk), (B, H, L)
+    table = [("q", q, keys, t, "r"), ("k", k, keys, t, "r"), ("v", v, (B, H, L, dv), t, "r"),
+             ("g", g, heads, torch.float32, "s"), ("beta", beta, heads, torch.float32, "s")]
     if lens is not None:
-        table["lens"] = (lens, (B,), torch.int32)
+        table.append(("lens", lens, (B,), torch.int32, "c"))
     return B, H, Hk, L, dk, dv, table
 
 
@@ -523,22 +545,14 @@ def infini_attn_gated_delta_forward(q, k, v, g, beta, S, out, scale: float = 0.0
     S [B,H,dk,dv] fp32, updated in place; lens: optional int32 [B] of row lengths on the device."""
     where = "infini_attn_gated_delta_forward"
     B, H, Hk, L, dk, dv, table = _gated_delta_shapes(where, q, k, v, g, beta, lens)
-    table["S"] = (S, (B, H, dk, dv), torch.float32)
-    table["out"] = (out, (B, H, L, dv), q.dtype)
+    table += [("S", S, (B, H, dk, dv), torch.float32, "c"), ("out", out, (B, H, L, dv), q.dtype, "r")]
     dev = _tensors(where, table)
-    _contiguous(where, S=S, lens=lens)
-    _rows_contiguous(where, q=q, k=k, v=v, out=out)
-    p = GatedDeltaParams()
-    p.q, p.k, p.v, p.g, p.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
-    p.S, p.out, p.lens = S.data_ptr(), out.data_ptr(), _ptr(lens)
-    p.B, p.H, p.Hk, p.L, p.dk, p.dv = B, H, Hk, L, dk, dv
-    p.mode, p.scale = _mode(0, q), float(scale)
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", out), ("g", g), ("beta", beta)):
-        getattr(p, f"{name}_stride")[:] = t.stride()[:3]
-    _workspace(where, p, workspace)
-    with torch.cuda.device(dev):
-        p.stream = _stream(stream)
-        rc = lib.infini_attn_gated_delta_forward(ctypes.byref(p))
+    space = _space(where, workspace, dev)
+    with _device(dev):
+        rc = lib.infini_attn_gated_delta_forward(_GD_FORWARD.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(), out.data_ptr(),
+            _at(lens), B, H, Hk, L, dk, dv, _mode(0, q), scale, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3],
+            *out.stride()[:3], *g.stride(), *beta.stride(), *space, _stream_on(stream, dev)))
     return _check(rc, where, raise_on_error)
 
 
@@ -556,30 +570,20 @@ def infini_attn_gated_delta_backward(q, k, v, g, beta, d_out, S0=None, dS_L=None
     others fp32; dS0 is None unless ``want_state_grad``.  Layouts as for the forward, d_out like out."""
     where = "infini_attn_gated_delta_backward"
     B, H, Hk, L, dk, dv, table = _gated_delta_shapes(where, q, k, v, g, beta, lens)
-    table["d_out"] = (d_out, (B, H, L, dv), q.dtype)
-    for name, t in (("S0", S0), ("dS_L", dS_L)):
-        if t is not None:
-            table[name] = (t, (B, H, dk, dv), torch.float32)
+    f32 = torch.float32
+    table.append(("d_out", d_out, (B, H, L, dv), q.dtype, "r"))
+    table += [(name, t, (B, H, dk, dv), f32, "c") for name, t in (("S0", S0), ("dS_L", dS_L)) if t is not None]
     dev = _tensors(where, table)
-    _contiguous(where, S0=S0, dS_L=dS_L, lens=lens)
-    _rows_contiguous(where, q=q, k=k, v=v, d_out=d_out)
-    p = GatedDeltaBackwardParams()
-    p.q, p.k, p.v, p.g, p.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
-    p.S0, p.d_out, p.dS_L, p.lens = _ptr(S0), d_out.data_ptr(), _ptr(dS_L), _ptr(lens)
-    p.B, p.H, p.Hk, p.L, p.dk, p.dv = B, H, Hk, L, dk, dv
-    p.mode, p.scale = _mode(0, q), float(scale)
-    for name, t in (("q", q), ("k", k), ("v", v), ("d_out", d_out), ("g", g), ("beta", beta)):
-        getattr(p, f"{name}_stride")[:] = t.stride()[:3]
-    _workspace(where, p, workspace)
-    with torch.cuda.device(dev), _on(stream):
-        new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-        dq, dkk, dvv = new(B, Hk, L, dk, dtype=q.dtype), new(B, Hk, L, dk, dtype=q.dtype), new(B, H, L, dv, dtype=q.dtype)
-        dg, dbeta = new(B, H, L), new(B, H, L)
-        dS0 = new(B, H, dk, dv) if want_state_grad else None
-        p.dq, p.dk_out, p.dv_out = dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr()
-        p.dg, p.dbeta, p.dS0 = dg.data_ptr(), dbeta.data_ptr(), _ptr(dS0)
-        p.stream = _stream(stream)
-        rc = lib.infini_attn_gated_delta_backward(ctypes.byref(p))
+    space = _space(where, workspace, dev)
+    with _device(dev), _on(stream):
+        dq, dkk, dvv = q.new_empty((B, Hk, L, dk)), q.new_empty((B, Hk, L, dk)), q.new_empty((B, H, L, dv))
+        dg, dbeta = g.new_empty((B, H, L)), g.new_empty((B, H, L))
+        dS0 = g.new_empty((B, H, dk, dv)) if want_state_grad else None
+        rc = lib.infini_attn_gated_delta_backward(_GD_BACKWARD.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _at(S0), d_out.data_ptr(), _at(dS_L),
+            _at(lens), dq.data_ptr(), dkk.data_ptr(), dvv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _at(dS0),
+            B, H, Hk, L, dk, dv, _mode(0, q), scale, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3],
+            *d_out.stride()[:3], *g.stride(), *beta.stride(), *space, _stream_on(stream, dev)))
     _check(rc, where, raise_on_error)
     return dq, dkk, dvv, dg, dbeta, dS0
 
@@ -602,39 +606,31 @@ def infini_attn_gated_delta_step(q_t, k_t, v_t, g, beta, S, out, slots=None, sca
         raise ValueError(f"{where}: q_t and v_t must have 3 dimensions and S 4")
     B, Hk, dk = q_t.shape
     H, dv = v_t.shape[1], v_t.shape[2]
-    f32 = torch.float32
-    table = dict(q_t=(q_t, (B, Hk, dk), t), k_t=(k_t, (B, Hk, dk), t), v_t=(v_t, (B, H, dv), t), g=(g, (B, H), f32),
-                 beta=(beta, (B, H), f32), S=(S, (S.shape[0], H, dk, dv), f32), out=(out, (B, H, dv), t))
+    pool, f32 = S.shape[0], torch.float32
+    table = [("q_t", q_t, (B, Hk, dk), t, "r"), ("k_t", k_t, (B, Hk, dk), t, "r"), ("v_t", v_t, (B, H, dv), t, "r"),
+             ("g", g, (B, H), f32, "s"), ("beta", beta, (B, H), f32, "s"), ("S", S, (pool, H, dk, dv), f32, "c"),
+             ("out", out, (B, H, dv), t, "r")]
     if slots is not None:
-        table["slots"] = (slots, (B,), torch.int32)
+        table.append(("slots", slots, (B,), torch.int32, "c"))
     dev = _tensors(where, table)
-    _contiguous(where, S=S, slots=slots)
-    _rows_contiguous(where, q_t=q_t, k_t=k_t, v_t=v_t, out=out)
-    p = GatedDeltaStepParams()
-    p.q, p.k, p.v, p.g, p.beta = q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), g.data_ptr(), beta.data_ptr()
-    p.S, p.out, p.slots = S.data_ptr(), out.data_ptr(), _ptr(slots)
-    p.B, p.H, p.Hk, p.pool, p.dk, p.dv = B, H, Hk, S.shape[0], dk, dv
-    p.mode, p.scale = _mode(0, q_t), float(scale)
-    for name, x in (("q", q_t), ("k", k_t), ("v", v_t), ("o", out), ("g", g), ("beta", beta)):
-        getattr(p, f"{name}_stride")[:] = x.stride()[:2]
-    with torch.cuda.device(dev):
-        p.stream = _stream(stream)
-        rc = lib.infini_attn_gated_delta_step(ctypes.byref(p))
+    with _device(dev):
+        rc = lib.infini_attn_gated_delta_step(_GD_STEP.pack(
+            q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(), out.data_ptr(),
+            _at(slots), B, H, Hk, pool, dk, dv, _mode(0, q_t), scale, *q_t.stride()[:2], *k_t.stride()[:2],
+            *v_t.stride()[:2], *out.stride()[:2], *g.stride(), *beta.stride(), _stream_on(stream, dev)))
     return _check(rc, where, raise_on_error)
 
 
-def _layer_norm_args(where, x, weight, more):
+def _layer_norm_args(where, x, weight, name, other, bias):
     t = _elem(where, x)
     if x.dim() < 1 or x.shape[-1] == 0:
         raise ValueError(f"{where}: x must have a last dimension to normalise")
     D = x.shape[-1]
     wt = _elem(where, weight)
-    table = dict(x=(x, x.shape, t), weight=(weight, (D,), wt))
-    for name, v in more.items():
-        if v is not None:
-            table[name] = (v, (D,), wt) if name == "bias" else (v, x.shape, t)
+    table = [("x", x, x.shape, t, "c"), ("weight", weight, (D,), wt, "c"), (name, other, x.shape, t, "c")]
+    if bias is not None:
+        table.append(("bias", bias, (D,), wt, "c"))
     dev = _tensors(where, table)
-    _contiguous(where, x=x, weight=weight, **more)
     return D, x.numel() // D, _mode(0, x) | (WEIGHT_F32 if wt == torch.float32 else 0), dev
 
 
@@ -642,10 +638,10 @@ def infini_attn_layer_norm_forward(x, weight, bias, y, eps: float = 1e-5, stream
     """y = (x - mean) / sqrt(var + eps) * weight + bias over the last dimension: x, y [..., D] contiguous, bf16 or
     fp32 (y may be x); weight, bias [D] bf16 or fp32, bias may be None."""
     where = "infini_attn_layer_norm_forward"
-    D, rows, mode, dev = _layer_norm_args(where, x, weight, dict(bias=bias, y=y))
-    with torch.cuda.device(dev):
+    D, rows, mode, dev = _layer_norm_args(where, x, weight, "y", y, bias)
+    with _device(dev):
         rc = lib.infini_attn_layer_norm_forward(x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), rows, D,
-                                                float(eps), mode, _stream(stream))
+                                                eps, mode, _stream_on(stream, dev))
     return _check(rc, where, raise_on_error)
 
 
@@ -654,15 +650,14 @@ def infini_attn_layer_norm_backward(x, weight, d_y, eps: float = 1e-5, want_bias
     """Gradients of infini_attn_layer_norm_forward: returns (dx, dweight, dbias) as new device tensors (dbias is
     None unless ``want_bias``); x, d_y [..., D] contiguous, one type; dweight, dbias in weight's type."""
     where = "infini_attn_layer_norm_backward"
-    D, rows, mode, dev = _layer_norm_args(where, x, weight, dict(d_y=d_y))
-    p = GatedDeltaParams()
-    _workspace(where, p, workspace)
-    with torch.cuda.device(dev), _on(stream):
+    D, rows, mode, dev = _layer_norm_args(where, x, weight, "d_y", d_y, None)
+    space = _space(where, workspace, dev)
+    with _device(dev), _on(stream):
         dx, dw = torch.empty_like(x), torch.empty_like(weight)
         db = torch.empty_like(weight) if want_bias else None
         rc = lib.infini_attn_layer_norm_backward(x.data_ptr(), weight.data_ptr(), d_y.data_ptr(), dx.data_ptr(),
-                                                 dw.data_ptr(), _ptr(db), rows, D, float(eps), mode, p.workspace,
-                                                 p.workspace_bytes, _stream(stream))
+                                                 dw.data_ptr(), _ptr(db), rows, D, eps, mode, *space,
+                                                 _stream_on(stream, dev))
     _check(rc, where, raise_on_error)
     return dx, dw, db
 

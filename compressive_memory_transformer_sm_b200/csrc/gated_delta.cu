@@ -119,6 +119,8 @@ struct ChunkSpace {
   }
 };
 
+constexpr int kMaxSmem = 232448;  // per block
+
 // The forward works through a long sequence in slabs of chunks, so that its workspace stays below this.
 constexpr size_t kSlabBytes = size_t(1) << 30;
 long long all_chunks(const Shape& s) { return (s.L + kC - 1) / kC; }
@@ -127,18 +129,26 @@ long long slab_chunks(const Shape& s) {
   return std::max<long long>(1, std::min<long long>(all_chunks(s), (long long)(kSlabBytes / one)));
 }
 
-// The dynamic shared-memory limit is an attribute of a function in the current context.
-template <typename F> int allow_smem(F* kernel, size_t bytes) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  return e == cudaSuccess ? INFINI_OK : note_cuda_error(e);
-}
-template <typename F> int launch_chunk(F* kernel, dim3 grid, int threads, size_t smem, int phase, const ChunkArgs& a, cudaStream_t st) {
-  const int rc = allow_smem(kernel, smem);
-  if (rc != INFINI_OK) return rc;
+// The dynamic shared-memory limit is an attribute of a function in the current context: raised to all there is once for
+// every context (and thread).
+template <typename... A> int launch_chunk(void (*kernel)(A...), dim3 grid, int threads, size_t smem, int phase, const ChunkArgs& a,
+                                          unsigned long long* raised, cudaStream_t st) {
+  const unsigned long long ctx = current_context_id();
+  if (ctx == 0 || *raised != ctx) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return note_cuda_error(e);
+    *raised = ctx;
+  }
   LaunchScope scope(phase, st);
   kernel<<<grid, threads, smem, st>>>(a);
   return launch_status();
 }
+// (kernel, grid, threads, shared memory, phase, arguments, stream), with the kernel's own note of the context
+#define GD_LAUNCH(kernel, grid, threads, smem, phase, a, st)              \
+  [&] {                                                                   \
+    static thread_local unsigned long long raised = 0;                    \
+    return launch_chunk(kernel, grid, threads, smem, phase, a, &raised, st); \
+  }()
 
 // Shape of a state block.  KS 4: four warps to 16 value columns, for the shortest time per chunk; KS 1: one warp, less
 // exchange, for the most chunks per SM.  As few groups per block as keep the blocks within one per SM.
@@ -154,7 +164,7 @@ template <typename T, int DK, int PP> StatePlan state_plan(int nw, long long hea
   while (p.groups < most && p.groups < nw && heads * ((nw + p.groups - 1) / p.groups) > kSms) p.groups *= 2;
   p.blocks = (nw + p.groups - 1) / p.groups;
   const size_t ex = p.KS == 4 ? p.groups * sizeof(Exchange<DK, Dims<T, DK>::kOut>) : 0;
-  p.stages = 2 * stage_bytes<T, DK, PP>(p.groups) + ex <= 232448 ? 2 : 1;
+  p.stages = 2 * stage_bytes<T, DK, PP>(p.groups) + ex <= (size_t)kMaxSmem ? 2 : 1;
   p.smem = p.stages * stage_bytes<T, DK, PP>(p.groups) + ex;
   // four more warps to copy, where the register file has room and the copies would take a large part of a chunk's time
   const bool loaders = p.KS == 4 ? p.groups < 4 && p.stages == 2 : p.groups == 1;
@@ -165,7 +175,7 @@ template <typename T, int DK, int PP> StatePlan state_plan(int nw, long long hea
 }
 
 template <typename T, int DK, int PP> int run_prep(const ChunkArgs& a, cudaStream_t st) {
-  return launch_chunk(prep_kernel<T, DK, PP>, dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
+  return GD_LAUNCH((prep_kernel<T, DK, PP>), dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
 }
 template <typename T, int DK> int chunk_forward(ChunkArgs a, long long chunks, long long slab, cudaStream_t st) {
   constexpr int PP = Dims<T, DK>::kOut;
@@ -179,8 +189,8 @@ template <typename T, int DK> int chunk_forward(ChunkArgs a, long long chunks, l
     a.nc = (int)std::min(slab, chunks - c);
     int rc = run_prep<T, DK, PP>(a, st);
     if (rc == INFINI_OK)
-      rc = p.KS == 4 ? launch_chunk(forward_kernel<T, DK, 4>, grid, p.threads, p.smem, kPhaseState, a, st)
-                     : launch_chunk(forward_kernel<T, DK, 1>, grid, p.threads, p.smem, kPhaseState, a, st);
+      rc = p.KS == 4 ? GD_LAUNCH((forward_kernel<T, DK, 4>), grid, p.threads, p.smem, kPhaseState, a, st)
+                     : GD_LAUNCH((forward_kernel<T, DK, 1>), grid, p.threads, p.smem, kPhaseState, a, st);
     if (rc != INFINI_OK) return rc;
   }
   return INFINI_OK;
@@ -193,14 +203,14 @@ template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
   a.stages = p.stages;
   a.first_loader = p.first_loader;
   const dim3 grid(2 * p.blocks, a.H, a.B);
-  rc = p.KS == 4 ? launch_chunk(both_kernel<T, DK, 4>, grid, p.threads, p.smem, kPhaseBwd, a, st)
-                 : launch_chunk(both_kernel<T, DK, 1>, grid, p.threads, p.smem, kPhaseBwd, a, st);
+  rc = p.KS == 4 ? GD_LAUNCH((both_kernel<T, DK, 4>), grid, p.threads, p.smem, kPhaseBwd, a, st)
+                 : GD_LAUNCH((both_kernel<T, DK, 1>), grid, p.threads, p.smem, kPhaseBwd, a, st);
   if (rc != INFINI_OK) return rc;
   const dim3 chunks(a.nc, a.Hk, a.B);
   if constexpr (sizeof(T) == 2)
-    return launch_chunk(grad_bf16_kernel<DK>, chunks, 512, sizeof(GradSmemB<DK>), kPhaseBwd, a, st);
+    return GD_LAUNCH((grad_bf16_kernel<DK>), chunks, 512, sizeof(GradSmemB<DK>), kPhaseBwd, a, st);
   else
-    return launch_chunk(grad_kernel<T, DK>, chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
+    return GD_LAUNCH((grad_kernel<T, DK>), chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
 }
 
 // Sequences of fewer tokens than this go token by token.

@@ -406,7 +406,7 @@ template <typename T> int dispatch(const Args& a, bool vec, bool bwd, cudaStream
     if (n <= 16) return launch<T, V, 16, 1>(a, bwd, st, parts);
     if (n <= 32) return launch<T, V, 32, 1>(a, bwd, st, parts);
     if (n <= 64) return launch<T, V, 32, 2>(a, bwd, st, parts);
-    if (n <= 128) return launch<T, V, 32, 4>(a, bwd, st, parts);
+    if (n <= 128) return launch<T, V, 64, 2>(a, bwd, st, parts);
     if (n <= 256) return launch<T, V, 128, 2>(a, bwd, st, parts);
     if (n <= 512) return launch<T, V, 256, 2>(a, bwd, st, parts);
     if (n <= 1024) return launch<T, V, 512, 2>(a, bwd, st, parts);

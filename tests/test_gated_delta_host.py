@@ -42,6 +42,15 @@ def test_struct_sizes():
     for which, cls in enumerate((api.GatedDeltaParams, api.GatedDeltaStepParams, api.GatedDeltaBackwardParams)):
         assert api.lib.infini_attn_gated_delta_params_size(which) == ctypes.sizeof(cls)
     assert api.lib.infini_attn_gated_delta_params_size(7) == 0
+    for packed, cls in ((api._GD_FORWARD, api.GatedDeltaParams), (api._GD_STEP, api.GatedDeltaStepParams),
+                        (api._GD_BACKWARD, api.GatedDeltaBackwardParams)):
+        n = sum(f[1]._length_ if hasattr(f[1], "_length_") else 1 for f in cls._fields_)
+        p = cls.from_buffer_copy(packed.pack(*range(1, n + 1)) + bytes(-packed.size % 8))
+        flat = []
+        for f, _ in cls._fields_:
+            x = getattr(p, f)
+            flat += list(x) if hasattr(x, "__len__") else [x]
+        assert flat == list(range(1, n + 1))
 
 
 def backward_params(**over):
@@ -159,6 +168,8 @@ def test_binding_refuses_what_it_cannot_pass_on():
         api.infini_attn_gated_delta_forward(q, k, v, g, g[:, :1], S, z(1, 2, 4, 8))
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         api.infini_attn_gated_delta_forward(q.half(), k, v, g, g, S, v)
+    with pytest.raises(ValueError, match="broadcast"):
+        api.infini_attn_gated_delta_forward(q, k, v, torch.tensor(0.0).expand(1, 2, 4), g, S, z(1, 2, 4, 8))
     with pytest.raises(TypeError):
         api.infini_attn_gated_delta_forward(q, None, v, g, g, S, v)
     with pytest.raises(ValueError, match="dimensions"):
