@@ -159,18 +159,16 @@ struct StatePlan {
 template <typename T, int DK, int PP> StatePlan state_plan(int nw, long long heads) {
   StatePlan p = {};
   p.KS = heads * nw <= 2 * kSms ? 4 : 1;
-  const int most = p.KS == 4 ? (sizeof(T) == 2 ? 4 : 2) : kMaxGroups;  // what fits in shared memory
+  const int most = p.KS == 4 ? 2 : kMaxGroups;
   p.groups = 1;
   while (p.groups < most && p.groups < nw && heads * ((nw + p.groups - 1) / p.groups) > kSms) p.groups *= 2;
   p.blocks = (nw + p.groups - 1) / p.groups;
-  const size_t ex = p.KS == 4 ? p.groups * sizeof(Exchange<DK, Dims<T, DK>::kOut>) : 0;
-  p.stages = 2 * stage_bytes<T, DK, PP>(p.groups) + ex <= (size_t)kMaxSmem ? 2 : 1;
-  p.smem = p.stages * stage_bytes<T, DK, PP>(p.groups) + ex;
-  // four more warps to copy, where the register file has room and the copies would take a large part of a chunk's time
-  const bool loaders = p.KS == 4 ? p.groups < 4 && p.stages == 2 : p.groups == 1;
-  const int work = 32 * p.KS * p.groups;
-  p.first_loader = loaders ? work : 0;
-  p.threads = loaders ? work + 128 : std::max(128, work);
+  const size_t one = stage_bytes<T, DK, PP>(p.groups), ex = p.KS == 4 ? p.groups * sizeof(Exchange<DK, Dims<T, DK>::kOut>) : 0;
+  const bool alone = heads * p.blocks <= kSms;  // a block per SM: two stages, and four warps that only copy
+  p.stages = alone && 2 * one + ex <= (size_t)kMaxSmem ? 2 : 1;
+  p.smem = p.stages * one + ex;
+  p.first_loader = alone ? std::max(128, 32 * p.KS * p.groups) : 0;
+  p.threads = alone ? p.first_loader + 128 : 32 * p.KS * p.groups;
   return p;
 }
 

@@ -109,6 +109,24 @@ template <int P> __device__ __forceinline__ BFrag<P> load_tri_n(const bf16* m, i
   for (int p = 0; p < P; ++p) ldsm4t(b.r[p], x + p * kTri);
   return b;
 }
+// ... of the 8-wide tiles ta and tb at k step kk, as B[k][n] = m[n][k] (blocks kk <= t / 2) and B[k][n] =
+// m[k][n] (kk >= t / 2); what a tile gets outside these blocks is not used.
+template <int P> __device__ __forceinline__ BFrag<P> load_tri_k2(const bf16* m, int ta, int tb, int kk, int lane) {
+  BFrag<P> b;
+  const int t = lane < 16 ? ta : tb, rb = t >> 1;
+  const bf16* x = m + tri_block(rb, min(kk, rb)) * 256 + tri_at((t & 1) * 8 + (lane & 7), lane & 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4(b.r[p], x + p * kTri);
+  return b;
+}
+template <int P> __device__ __forceinline__ BFrag<P> load_tri_n2(const bf16* m, int ta, int tb, int kk, int lane) {
+  BFrag<P> b;
+  const int t = lane < 16 ? ta : tb, cb = t >> 1;
+  const bf16* x = m + tri_block(max(kk, cb), cb) * 256 + tri_at(lane & 15, (t & 1) * 8);
+#pragma unroll
+  for (int p = 0; p < P; ++p) ldsm4t(b.r[p], x + p * kTri);
+  return b;
+}
 // A[m][k] = m[m][k] of block (rb, cb), and A[m][k] = m[k][m].
 template <int P> __device__ __forceinline__ AFrag<P> load_tri_a_k(const bf16* m, int rb, int cb, int lane) {
   AFrag<P> a;
@@ -145,14 +163,54 @@ template <int P> __device__ __forceinline__ void put_parts(bf16* dst, int plane,
 
 // ------------------------------------------------------------------ prep
 template <typename T, int DK> struct PrepSmem {
-  T k[kC * Dims<T, DK>::kLdK];
-  T q[kC * Dims<T, DK>::kLdK];
+  union {
+    struct {
+      T k[kC * Dims<T, DK>::kLdK];
+      T q[kC * Dims<T, DK>::kLdK];
+    };
+    struct {  // once the products are done
+      float R[kC * kLdT];  // T
+      float E[3 * 256];
+    };
+  };
   float A[kC * kLdT];
-  float R[kC * kLdT];  // T
-  float E[6 * 256];
   double G[kC];
   float beta[kC];
 };
+
+// Blocks at distance D below the diagonal: T_rc = -T_rr (sum_(c <= m < r) A_rm T_mc), r = c + D; a thread per element.
+template <int D> __device__ __forceinline__ void invert_level(const float* A, float* R, float* E, int i, int j) {
+#pragma unroll
+  for (int c = 0; c < 4 - D; ++c) {
+    const int r = c + D;
+    float y = 0.f;
+#pragma unroll
+    for (int m = 16 * c; m < 16 * r; m += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(A + (16 * r + i) * kLdT + m);
+      y = fmaf(x.x, R[m * kLdT + 16 * c + j], y);
+      y = fmaf(x.y, R[(m + 1) * kLdT + 16 * c + j], y);
+      y = fmaf(x.z, R[(m + 2) * kLdT + 16 * c + j], y);
+      y = fmaf(x.w, R[(m + 3) * kLdT + 16 * c + j], y);
+    }
+    E[c * 256 + i * 16 + j] = y;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < 4 - D; ++c) {
+    const int r = c + D;
+    float y = 0.f;
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(R + (16 * r + i) * kLdT + 16 * r + m);
+      y = fmaf(-x.x, E[c * 256 + m * 16 + j], y);
+      y = fmaf(-x.y, E[c * 256 + (m + 1) * 16 + j], y);
+      y = fmaf(-x.z, E[c * 256 + (m + 2) * 16 + j], y);
+      y = fmaf(-x.w, E[c * 256 + (m + 3) * 16 + j], y);
+    }
+    R[(16 * r + i) * kLdT + 16 * c + j] = y;
+  }
+  __syncthreads();
+}
 
 // PP: parts of P that are stored
 template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) prep_kernel(const ChunkArgs a) {
@@ -249,29 +307,9 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
     }
   }
   __syncthreads();
-  // off the diagonal, by distance: T_rc = -T_rr (sum_(c <= m < r) A_rm T_mc)
-  for (int d = 1; d < 4; ++d) {
-    const int blocks = 4 - d, i = (tid >> 4) & 15, j = tid & 15;
-    float y[3] = {};
-#pragma unroll
-    for (int cb = 0; cb < 3; ++cb)
-      if (cb < blocks) {
-        const int r = cb + d;
-        for (int m = 16 * cb; m < 16 * r; ++m) y[cb] = fmaf(s.A[(16 * r + i) * kLdT + m], s.R[m * kLdT + 16 * cb + j], y[cb]);
-        s.E[cb * 256 + i * 16 + j] = y[cb];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int cb = 0; cb < 3; ++cb)
-      if (cb < blocks) {
-        const int r = cb + d;
-        float x = 0.f;
-#pragma unroll
-        for (int m = 0; m < 16; ++m) x = fmaf(-s.R[(16 * r + i) * kLdT + 16 * r + m], s.E[cb * 256 + m * 16 + j], x);
-        s.R[(16 * r + i) * kLdT + 16 * cb + j] = x;
-      }
-    __syncthreads();
-  }
+  invert_level<1>(s.A, s.R, s.E, tid >> 4, tid & 15);
+  invert_level<2>(s.A, s.R, s.E, tid >> 4, tid & 15);
+  invert_level<3>(s.A, s.R, s.E, tid >> 4, tid & 15);
   bf16* T_out = a.T + at * 3 * kTri;
   for (int i = tid; i < kTri / 2; i += 256) {
     const int blk = i >> 7, e = (i & 127) * 2;
@@ -282,7 +320,7 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
 }
 
 // ------------------------------------------------------------------ state
-constexpr int kMaxGroups = 8;
+constexpr int kMaxGroups = 4;
 template <typename T, int DK, int PP> struct Stage {
   T k[kC * Dims<T, DK>::kLdK];
   T q[kC * Dims<T, DK>::kLdK];
@@ -368,7 +406,7 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
   constexpr int NB = 4 / KS, ND = DK / KS / 8;  // token blocks and state tiles of a warp
   typedef Stage<T, DK, PP> St;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, c2 = 2 * (lane & 3);
   const int group = warp / KS, ks = warp % KS, ldv = strip_ld<T>(a.groups), nw = (a.dv + 15) >> 4;
   const int wg = group < a.groups ? vblock * a.groups + group : nw;  // 16 columns from v0
   const int v0 = 16 * wg, vb = 16 * vblock * a.groups, vs = 16 * group;
@@ -393,6 +431,8 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
                            tid - a.first_loader, nthr - a.first_loader);
   };
   const bool live = wg < nw;
+  // a warp's tiles of 8 tokens: all of them (KS 1), or tiles ks and 7 - ks, so that the triangular products balance
+  auto tile = [&](int x, int y) { return KS == 1 ? 2 * x + y : y ? 7 - ks : ks; };
   float S[ND][4];
   const float* from = OUT ? a.S : a.S0;
   state_load<ND>(S, from ? from + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
@@ -408,9 +448,10 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
     if (a.stages == 2 && i + 1 < nc) fetch(i + 1);
     St& s = *reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage);
     T* sv = reinterpret_cast<T*>(&s + 1);
+    auto vec2 = [&](int which, int t) { return *reinterpret_cast<const float2*>(s.vec + 64 * which + 8 * t + c2); };
     if (live) {
       if (!OUT) state_snap<ND>(S, a.snap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
-      // R^T = S^T K^T, Y^T = S^T Q^T: 16 tokens per block
+      // R^T = S^T K^T, Y^T = S^T Q^T
       float R[NB][2][4] = {}, Y[NB][2][4] = {}, lo[NB][2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
@@ -421,69 +462,80 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
           fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
-          const int blk = KS > 1 ? ks : x;
-          mma2(R[x][0], R[x][1], lo[x][0], lo[x][1], fs, load_b_k<PI>(s.k, LD, 16 * blk, 16 * kk, lane));
+          mma2(R[x][0], R[x][1], lo[x][0], lo[x][1], fs, load_b_k2(s.k, LD, tile(x, 0), tile(x, 1), 16 * kk, lane));
           if (OUT) {
             AFrag<PO> fo;
 #pragma unroll
             for (int p = 0; p < PO; ++p)
 #pragma unroll
               for (int y = 0; y < 4; ++y) fo.r[p][y] = fs.r[p][y];
-            mma2(Y[x][0], Y[x][1], fo, load_b_k<PI>(s.q, LD, 16 * blk, 16 * kk, lane));
+            mma2(Y[x][0], Y[x][1], fo, load_b_k2(s.q, LD, tile(x, 0), tile(x, 1), 16 * kk, lane));
           }
         }
       }
       // X^T = beta (V^T - gamma R^T), in R's place
 #pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        const int blk = KS > 1 ? ks : x;
+      for (int x = 0; x < NB; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile(x, y);
+          const float2 gam = vec2(0, t), be = vec2(2, t);
+          float v[4];
+          load_tile_t(v, sv + 8 * t * ldv + vs, ldv, lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int t = 16 * blk + 8 * y + c2 + (e & 1);
-            R[x][y][e] = s.vec[128 + t] * (to_f32(sv[t * ldv + vs + g + 8 * (e >> 1)]) - s.vec[t] * (R[x][y][e] + lo[x][y][e]));
+            R[x][y][e] = (e & 1 ? be.y : be.x) * (v[e] - (e & 1 ? gam.y : gam.x) * (R[x][y][e] + lo[x][y][e]));
             lo[x][y][e] = 0.f;
           }
-        if constexpr (KS > 1) put_frag<3>(ex.X[blk][0], from_acc<3>(R[x][0], R[x][1]), lane);
-      }
+          if constexpr (KS > 1) put_tile<3>(ex.X[t >> 1][0], R[x][y], t, lane);
+        }
       if constexpr (KS > 1) group_sync<KS>(group);
       // U^T = X^T T^T
       float U[NB][2][4] = {};
+      if constexpr (KS > 1) {  // every fragment first: the loads overlap, only the products branch
+        AFrag<3> fx[4];
+        BFrag<3> ft[4];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (KS > 1 && kk > ks) break;
-        AFrag<3> fx;
-        if constexpr (KS > 1)
-          fx = get_frag<3>(ex.X[kk][0], lane);
-        else
-          fx = from_acc<3>(R[kk][0], R[kk][1]);
+        for (int kk = 0; kk < 4; ++kk) {
+          fx[kk] = get_frag<3>(ex.X[kk][0], lane);
+          ft[kk] = load_tri_k2<3>(s.Tm, tile(0, 0), tile(0, 1), kk, lane);
+        }
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          const int blk = KS > 1 ? ks : x;
-          if (KS > 1 || blk >= kk)
-            mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fx, load_tri_k<3>(s.Tm, blk, kk, lane));
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk <= tile(0, 0) >> 1)
+            mma2(U[0][0], U[0][1], lo[0][0], lo[0][1], fx[kk], ft[kk]);
+          else if (kk <= tile(0, 1) >> 1)
+            mma1(U[0][1], lo[0][1], fx[kk], ft[kk], 1);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const AFrag<3> fx = from_acc<3>(R[kk][0], R[kk][1]);
+#pragma unroll
+          for (int x = kk; x < NB; ++x) mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fx, load_tri_k<3>(s.Tm, x, kk, lane));
         }
       }
       AFrag<3> fw[4];   // rho U
       AFrag<PO> fu[4];  // U
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        const int blk = KS > 1 ? ks : x;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile(x, y);
 #pragma unroll
           for (int e = 0; e < 4; ++e) U[x][y][e] += lo[x][y][e];
-        if (OUT) {
-          fu[x] = from_acc<PO>(U[x][0], U[x][1]);
-          if constexpr (KS > 1) put_frag<PO>(ex.U[blk][0], fu[x], lane);
+          if constexpr (OUT && KS > 1) put_tile<PO>(ex.U[t >> 1][0], U[x][y], t, lane);
         }
+        if constexpr (OUT && KS == 1) fu[x] = from_acc<PO>(U[x][0], U[x][1]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile(x, y);
+          const float2 rho = vec2(1, t);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) U[x][y][e] *= s.vec[64 + 16 * blk + 8 * y + c2 + (e & 1)];
-        fw[x] = from_acc<3>(U[x][0], U[x][1]);
-        if constexpr (KS > 1) put_frag<3>(ex.W[blk][0], fw[x], lane);
+          for (int e = 0; e < 4; ++e) U[x][y][e] *= e & 1 ? rho.y : rho.x;
+          if constexpr (KS > 1) put_tile<3>(ex.W[t >> 1][0], U[x][y], t, lane);
+        }
+        if constexpr (KS == 1) fw[x] = from_acc<3>(U[x][0], U[x][1]);
       }
       if constexpr (KS > 1) {
         group_sync<KS>(group);
@@ -495,19 +547,35 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
 #pragma unroll
         for (int x = 0; x < NB; ++x)
 #pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 gam = vec2(0, tile(x, y));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Y[x][y][e] *= e & 1 ? gam.y : gam.x;
+          }
+        if constexpr (KS > 1) {
+          BFrag<PO> fp[4];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            fu[kk] = get_frag<PO>(ex.U[kk][0], lane);
+            fp[kk] = load_tri_k2<PO>(s.P, tile(0, 0), tile(0, 1), kk, lane);
+          }
+          float yl[2][4] = {};
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk <= tile(0, 0) >> 1)
+              mma2(Y[0][0], Y[0][1], yl[0], yl[1], fu[kk], fp[kk]);
+            else if (kk <= tile(0, 1) >> 1)
+              mma1(Y[0][1], yl[1], fu[kk], fp[kk], 1);
+          }
+#pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Y[x][y][e] *= s.vec[16 * (KS > 1 ? ks : x) + 8 * y + c2 + (e & 1)];
+            for (int e = 0; e < 4; ++e) Y[0][y][e] += yl[y][e];
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (KS > 1 && kk > ks) break;
-          if constexpr (KS > 1) fu[kk] = get_frag<PO>(ex.U[kk][0], lane);
+          for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-          for (int x = 0; x < NB; ++x) {
-            const int blk = KS > 1 ? ks : x;
-            if (KS > 1 || blk >= kk)
-              mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, blk, kk, lane));
-          }
+            for (int x = kk; x < NB; ++x) mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, x, kk, lane));
         }
         __syncwarp();  // every lane has taken its v
         const int n = chunk_len(len, a.c0 + i), w = min(16, a.dv - v0);
@@ -515,22 +583,23 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
 #pragma unroll
         for (int x = 0; x < NB; ++x)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+          for (int y = 0; y < 2; ++y) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sv[(16 * (KS > 1 ? ks : x) + 8 * y + c2 + (e & 1)) * ldv + vs + g + 8 * (e >> 1)] = from_f32<T>(a.scale * Y[x][y][e]);
+            for (int e = 0; e < 4; ++e) Y[x][y][e] *= a.scale;
+            store_tile_t(sv + 8 * tile(x, y) * ldv + vs, ldv, Y[x][y], lane);
+          }
         __syncwarp();
-        const int ta = KS > 1 ? 16 * ks : 0;
+        auto token = [&](int r) { return KS == 1 ? r : 8 * tile(0, r >> 3) + (r & 7); };  // of the warp's row r
         if (a.vec_o) {
           constexpr int V = 16 / sizeof(T), per = 16 / V;
 #pragma unroll
           for (int x = lane; x < 16 * NB * per; x += 32) {
-            const int t = ta + x / per, y = (x % per) * V;
+            const int t = token(x / per), y = (x % per) * V;
             if (t < n && y < w) *reinterpret_cast<uint4*>(o + t * a.os[2] + y) = *reinterpret_cast<const uint4*>(sv + t * ldv + vs + y);
           }
         } else {
           for (int x = lane; x < 16 * NB * 16; x += 32) {
-            const int t = ta + (x >> 4), y = x & 15;
+            const int t = token(x >> 4), y = x & 15;
             if (t < n && y < w) o[t * a.os[2] + y] = sv[t * ldv + vs + y];
           }
         }
@@ -585,6 +654,7 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
                           tid - a.first_loader, nthr - a.first_loader);
   };
   const bool live = wg < nw;
+  auto tile = [&](int x, int y) { return KS == 1 ? 2 * x + y : y ? 7 - ks : ks; };
   float S[ND][4];
   state_load<ND>(S, a.dS ? a.dS + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
   if (nc > 0) fetch(nc - 1);
@@ -599,6 +669,7 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
     if (a.stages == 2 && i > 0) fetch(i - 1);
     St& s = *reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage);
     const T* sd = reinterpret_cast<const T*>(&s + 1);
+    auto vec2 = [&](int which, int t) { return *reinterpret_cast<const float2*>(s.vec + 64 * which + 8 * t + c2); };
     if (live) {
       state_snap<ND>(S, a.dsnap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // dU^T = scale dO^T P + rho (dS^T K^T)
@@ -612,72 +683,94 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
           fs = from_acc<3>(S[2 * kk], S[2 * kk + 1]);
 #pragma unroll
         for (int x = 0; x < NB; ++x)
-          mma2(W[x][0], W[x][1], lw[x][0], lw[x][1], fs, load_b_k<PI>(s.k, LD, 16 * (KS > 1 ? ks : x), 16 * kk, lane));
+          mma2(W[x][0], W[x][1], lw[x][0], lw[x][1], fs, load_b_k2(s.k, LD, tile(x, 0), tile(x, 1), 16 * kk, lane));
       }
+      if constexpr (KS > 1) {  // every fragment first: the loads overlap, only the products branch
+        AFrag<PI> fd[4];
+        BFrag<3> fp[4];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (KS > 1 && kk < ks) continue;
-        const AFrag<PI> fd = load_a_m<PI>(sd, ldv, 16 * kk, vs, lane);
+        for (int kk = 0; kk < 4; ++kk) {
+          fd[kk] = load_a_m<PI>(sd, ldv, 16 * kk, vs, lane);
+          fp[kk] = load_tri_n2<3>(s.P, tile(0, 0), tile(0, 1), kk, lane);
+        }
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          const int blk = KS > 1 ? ks : x;
-          if (KS > 1 || blk <= kk)
-            mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fd, load_tri_n<3>(s.P, kk, blk, lane));
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk >= tile(0, 1) >> 1)
+            mma2(U[0][0], U[0][1], lo[0][0], lo[0][1], fd[kk], fp[kk]);
+          else if (kk >= tile(0, 0) >> 1)
+            mma1(U[0][0], lo[0][0], fd[kk], fp[kk], 0);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const AFrag<PI> fd = load_a_m<PI>(sd, ldv, 16 * kk, vs, lane);
+#pragma unroll
+          for (int x = 0; x <= kk; ++x)
+            if (x < NB) mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fd, load_tri_n<3>(s.P, kk, x, lane));
         }
       }
 #pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        const int blk = KS > 1 ? ks : x;
+      for (int x = 0; x < NB; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile(x, y);
+          const float2 rho = vec2(1, t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            U[x][y][e] = a.scale * (U[x][y][e] + lo[x][y][e]) +
-                         s.vec[64 + 16 * blk + 8 * y + c2 + (e & 1)] * (W[x][y][e] + lw[x][y][e]);
+            U[x][y][e] = a.scale * (U[x][y][e] + lo[x][y][e]) + (e & 1 ? rho.y : rho.x) * (W[x][y][e] + lw[x][y][e]);
             W[x][y][e] = lo[x][y][e] = 0.f;
           }
-        if constexpr (KS > 1) put_frag<3>(ex.X[blk][0], from_acc<3>(U[x][0], U[x][1]), lane);
-      }
+          if constexpr (KS > 1) put_tile<3>(ex.X[t >> 1][0], U[x][y], t, lane);
+        }
       if constexpr (KS > 1) group_sync<KS>(group);
       // dX^T = dU^T T, then -beta gamma dX^T
+      if constexpr (KS > 1) {
+        AFrag<3> fx[4];
+        BFrag<3> ft[4];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (KS > 1 && kk < ks) continue;
-        AFrag<3> fx;
-        if constexpr (KS > 1)
-          fx = get_frag<3>(ex.X[kk][0], lane);
-        else
-          fx = from_acc<3>(U[kk][0], U[kk][1]);
+        for (int kk = 0; kk < 4; ++kk) {
+          fx[kk] = get_frag<3>(ex.X[kk][0], lane);
+          ft[kk] = load_tri_n2<3>(s.Tm, tile(0, 0), tile(0, 1), kk, lane);
+        }
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          const int blk = KS > 1 ? ks : x;
-          if (KS > 1 || blk <= kk)
-            mma2(W[x][0], W[x][1], lo[x][0], lo[x][1], fx, load_tri_n<3>(s.Tm, kk, blk, lane));
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk >= tile(0, 1) >> 1)
+            mma2(W[0][0], W[0][1], lo[0][0], lo[0][1], fx[kk], ft[kk]);
+          else if (kk >= tile(0, 0) >> 1)
+            mma1(W[0][0], lo[0][0], fx[kk], ft[kk], 0);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const AFrag<3> fx = from_acc<3>(U[kk][0], U[kk][1]);
+#pragma unroll
+          for (int x = 0; x <= kk; ++x)
+            if (x < NB) mma2(W[x][0], W[x][1], lo[x][0], lo[x][1], fx, load_tri_n<3>(s.Tm, kk, x, lane));
         }
       }
       AFrag<3> fw[4];
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        const int blk = KS > 1 ? ks : x;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile(x, y);
+          const float2 gam = vec2(0, t), be = vec2(2, t);
+          const float f[2] = {-be.x * gam.x, -be.y * gam.y};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = 16 * blk + 8 * y + c2 + (e & 1);
-            W[x][y][e] = -s.vec[128 + t] * s.vec[t] * (W[x][y][e] + lo[x][y][e]);
-          }
-        fw[x] = from_acc<3>(W[x][0], W[x][1]);
-        if constexpr (KS > 1) put_frag<3>(ex.W[blk][0], fw[x], lane);
+          for (int e = 0; e < 4; ++e) W[x][y][e] = f[e & 1] * (W[x][y][e] + lo[x][y][e]);
+          if constexpr (KS > 1) put_tile<3>(ex.W[t >> 1][0], W[x][y], t, lane);
+        }
+        if constexpr (KS == 1) fw[x] = from_acc<3>(W[x][0], W[x][1]);
       }
+      AFrag<3> fd[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) fd[kk] = load_a_m_scaled<3>(sd, ldv, 16 * kk, vs, lane, s.vec + 16 * kk, a.scale);
       if constexpr (KS > 1) {
         group_sync<KS>(group);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) fw[kk] = get_frag<3>(ex.W[kk][0], lane);
       }
       const float full = s.vec[192];
-      AFrag<3> fd[4];
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) fd[kk] = load_a_m_scaled<3>(sd, ldv, 16 * kk, vs, lane, s.vec + 16 * kk, a.scale);
 #pragma unroll
       for (int np = 0; np < ND / 2; ++np) {
         float hi[2][4] = {}, l2[2][4] = {};
@@ -700,7 +793,8 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
   if (a.dS0 && live) state_store<ND>(S, a.dS0 + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
 }
 
-constexpr int state_threads(int KS) { return KS == 4 ? 512 : 256; }  // at most
+// Threads at most: two (KS 4) or four (KS 1) groups and four copying warps.
+constexpr int state_threads(int KS) { return KS == 4 ? 384 : 256; }
 
 template <typename T, int DK, int KS> __global__ void __launch_bounds__(state_threads(KS)) forward_kernel(const ChunkArgs a) {
   state_pass<T, DK, KS, true, Dims<T, DK>::kOut>(a, blockIdx.x, blockIdx.y, blockIdx.z);

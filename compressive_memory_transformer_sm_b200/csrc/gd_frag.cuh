@@ -47,10 +47,22 @@ template <int PA, int PB> __device__ __forceinline__ void mma2(float (&d0)[4], f
     }
 }
 
-// The same with the pairs of order above 0 (2^-8 of the result) in sums of their own: the tensor
-// cores truncate each addition to a running sum, so the fewer additions the large sum takes the
-// smaller the error (the state over 512 chunks, relative: 3.6e-7 before, 2.0e-7 so), and the sums are
-// independent chains.
+// Column tile t of d += A B with the pairs of order above 0 (2^-8 of the result) in a sum of their
+// own: the tensor cores truncate each addition to a running sum, so the fewer additions the large
+// sum takes the smaller the error (the state over 512 chunks, relative: 3.6e-7 before, 2.0e-7 so),
+// and the sums are independent chains.
+template <int PA, int PB> __device__ __forceinline__ void mma1(float (&h)[4], float (&l)[4], const AFrag<PA>& a, const BFrag<PB>& b, int t) {
+  constexpr int M = (PA > PB ? PA : PB) - 1;
+  mma16816(h, a.r[0], b.r[0][2 * t], b.r[0][2 * t + 1]);
+#pragma unroll
+  for (int o = M; o > 0; --o)
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int j = o - i;
+      if (j >= 0 && j < PB) mma16816(l, a.r[i], b.r[j][2 * t], b.r[j][2 * t + 1]);
+    }
+}
+// Both tiles.
 template <int PA, int PB>
 __device__ __forceinline__ void mma2(float (&h0)[4], float (&h1)[4], float (&l0)[4], float (&l1)[4], const AFrag<PA>& a, const BFrag<PB>& b) {
   constexpr int M = (PA > PB ? PA : PB) - 1;
@@ -116,6 +128,23 @@ template <int P> __device__ __forceinline__ BFrag<P> load_b_k(const float* m, in
     for (int h = 0; h < 2; ++h) {
       const float2 x = *reinterpret_cast<const float2*>(p + 8 * t * ld + 8 * h);
       split<P>(x.x, x.y, b.r, 2 * t + h);
+    }
+  return b;
+}
+// ... columns of the tiles ta and tb (8 each)
+__device__ __forceinline__ BFrag<1> load_b_k2(const bf16* m, int ld, int ta, int tb, int k0, int lane) {
+  BFrag<1> b;
+  ldsm4(b.r[0], m + ((lane < 16 ? ta : tb) * 8 + (lane & 7)) * ld + k0 + (lane & 8));
+  return b;
+}
+__device__ __forceinline__ BFrag<3> load_b_k2(const float* m, int ld, int ta, int tb, int k0, int lane) {
+  BFrag<3> b;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = *reinterpret_cast<const float2*>(m + ((t ? tb : ta) * 8 + (lane >> 2)) * ld + k0 + 2 * (lane & 3) + 8 * h);
+      split<3>(x.x, x.y, b.r, 2 * t + h);
     }
   return b;
 }
@@ -252,6 +281,44 @@ template <int P> __device__ __forceinline__ BFrag<P> b_from_acc(const float4& t0
 template <int P> __device__ __forceinline__ void put_frag(uint4* dst, const AFrag<P>& a, int lane) {
 #pragma unroll
   for (int p = 0; p < P; ++p) dst[p * 32 + lane] = make_uint4(a.r[p][0], a.r[p][1], a.r[p][2], a.r[p][3]);
+}
+// ... the half of k step t / 2 that accumulator tile t is
+template <int P> __device__ __forceinline__ void put_tile(uint4* dst, const float (&x)[4], int t, int lane) {
+  uint32_t r[P][4];
+  split<P>(x[0], x[1], r, 0);
+  split<P>(x[2], x[3], r, 1);
+#pragma unroll
+  for (int p = 0; p < P; ++p) reinterpret_cast<uint2*>(dst + p * 32 + lane)[t & 1] = make_uint2(r[p][0], r[p][1]);
+}
+// A [16 columns x 8 tokens] accumulator tile (rows = columns of m) from, and rounded to, 8 rows of m from x.
+__device__ __forceinline__ void load_tile_t(float (&d)[4], const float* m, int ld, int lane) {
+  const float* p = m + 2 * (lane & 3) * ld + (lane >> 2);
+  d[0] = p[0];
+  d[1] = p[ld];
+  d[2] = p[8];
+  d[3] = p[ld + 8];
+}
+__device__ __forceinline__ void load_tile_t(float (&d)[4], const bf16* m, int ld, int lane) {
+  uint32_t a, b;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+               : "=r"(a), "=r"(b)
+               : "r"(smem_u32(m + (lane & 7) * ld + (lane & 8))));
+  d[0] = bf16_lo(a);
+  d[1] = bf16_hi(a);
+  d[2] = bf16_lo(b);
+  d[3] = bf16_hi(b);
+}
+__device__ __forceinline__ void store_tile_t(float* m, int ld, const float (&d)[4], int lane) {
+  float* p = m + 2 * (lane & 3) * ld + (lane >> 2);
+  p[0] = d[0];
+  p[ld] = d[1];
+  p[8] = d[2];
+  p[ld + 8] = d[3];
+}
+__device__ __forceinline__ void store_tile_t(bf16* m, int ld, const float (&d)[4], int lane) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(smem_u32(m + (lane & 7) * ld + (lane & 8))),
+               "r"(pack_bf16x2(d[0], d[1])), "r"(pack_bf16x2(d[2], d[3]))
+               : "memory");
 }
 template <int P> __device__ __forceinline__ AFrag<P> get_frag(const uint4* src, int lane) {
   AFrag<P> a;
