@@ -112,7 +112,7 @@ struct ChunkSpace {
     a.T = reinterpret_cast<bf16*>(w + T);
     a.P = reinterpret_cast<bf16*>(w + P);
     a.vec = reinterpret_cast<float*>(w + vec);
-    a.G = reinterpret_cast<double*>(w + G);
+    a.G = reinterpret_cast<float2*>(w + G);
     a.snap = reinterpret_cast<float4*>(w + snap);
     a.dsnap = reinterpret_cast<float4*>(w + dsnap);
     a.acc = reinterpret_cast<float*>(w + acc);

@@ -67,7 +67,7 @@ struct ChunkArgs {
   bf16* T;       // [B H][nc][3][kTri]: the three bf16 parts
   bf16* P;       // [B H][nc][parts][kTri]
   float* vec;    // [B H][nc][kVec]
-  double* G;     // [B H][nc][64]
+  float2* G;     // [B H][nc][64]: high and low part
   float4* snap;  // [B H][nc][nw][DK / 8][32]: states before the chunks (accumulator order)
   float4* dsnap; // the same of the gradients of the states after them
   float* S;      // state_kernel: [B, H, dk, dv] read and written; grad: unused
@@ -83,6 +83,19 @@ struct ChunkArgs {
   bool vec_dq, vec_dv;  // pairs of dq and dk, 16-byte rows of dv can be written whole
   float* acc;  // grad, group > 1: [B Hk][nc][2][64][DK] running sums over the value heads of a key head
 };
+
+// A sum of log decays as two floats, and e^(a - b) of two such sums where `in`, else 0.  The
+// difference of the high parts rounds at 2^-24 of itself and the low parts hold what they lack, so
+// this is as good as a difference in 64 bits, whose conversions cost 6000 of 17000 cycles of a
+// chunk's preparation; no branch, so that the exponentials overlap.
+__device__ __forceinline__ float2 halves(double x) {
+  const float hi = (float)x;
+  return make_float2(hi, (float)(x - hi));
+}
+__device__ __forceinline__ float decay(float2 a, float2 b, bool in) {
+  const float e = expf(in ? (a.x - b.x) + (a.y - b.y) : 0.f);
+  return in ? e : 0.f;
+}
 
 __device__ __forceinline__ long long row_len(const ChunkArgs& a, int b) {
   return a.lens ? min(max((long long)a.lens[b], 0LL), a.L) : a.L;
@@ -168,48 +181,43 @@ template <typename T, int DK> struct PrepSmem {
       T k[kC * Dims<T, DK>::kLdK];
       T q[kC * Dims<T, DK>::kLdK];
     };
-    struct {  // once the products are done
-      float R[kC * kLdT];  // T
-      float E[3 * 256];
-    };
+    float R[kC * kLdT];  // T, once the products are done
   };
   float A[kC * kLdT];
-  double G[kC];
+  float2 G[kC];
   float beta[kC];
 };
 
-// Blocks at distance D below the diagonal: T_rc = -T_rr (sum_(c <= m < r) A_rm T_mc), r = c + D; a thread per element.
-template <int D> __device__ __forceinline__ void invert_level(const float* A, float* R, float* E, int i, int j) {
+// Blocks at distance D below the diagonal: T_rc = -T_rr (sum_(c <= m < r) A_rm T_mc), r = c + D; warp c
+// computes its block, into R and in parts into T.  (Scalar products by all threads: 256 fused
+// multiply-adds and as many shared loads a thread, 4000 of 17000 cycles.)
+template <int D> __device__ __forceinline__ void invert_level(const float* A, float* R, bf16* T, int warp, int lane) {
+  const int c = warp, r = c + D, g = lane >> 2, c2 = 2 * (lane & 3);
+  if (c < 4 - D) {
+    float hi[2][4] = {}, lo[2][4] = {};
 #pragma unroll
-  for (int c = 0; c < 4 - D; ++c) {
-    const int r = c + D;
-    float y = 0.f;
+    for (int m = 0; m < D; ++m)
+      mma2(hi[0], hi[1], lo[0], lo[1], load_a_k<3>(A, kLdT, 16 * r, 16 * (c + m), lane), load_b_n<3>(R, kLdT, 16 * (c + m), 16 * c, lane));
+    float4 e[2];
 #pragma unroll
-    for (int m = 16 * c; m < 16 * r; m += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(A + (16 * r + i) * kLdT + m);
-      y = fmaf(x.x, R[m * kLdT + 16 * c + j], y);
-      y = fmaf(x.y, R[(m + 1) * kLdT + 16 * c + j], y);
-      y = fmaf(x.z, R[(m + 2) * kLdT + 16 * c + j], y);
-      y = fmaf(x.w, R[(m + 3) * kLdT + 16 * c + j], y);
-    }
-    E[c * 256 + i * 16 + j] = y;
+    for (int t = 0; t < 2; ++t) e[t] = make_float4(hi[t][0] + lo[t][0], hi[t][1] + lo[t][1], hi[t][2] + lo[t][2], hi[t][3] + lo[t][3]);
+    const BFrag<3> fe = b_from_acc<3>(e[0], e[1]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) hi[t][x] = lo[t][x] = 0.f;
+    mma2(hi[0], hi[1], lo[0], lo[1], load_a_k<3>(R, kLdT, 16 * r, 16 * r, lane), fe);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x0 = -(hi[t][2 * h] + lo[t][2 * h]), x1 = -(hi[t][2 * h + 1] + lo[t][2 * h + 1]);
+        const int i = g + 8 * h, j = 8 * t + c2;
+        if (D < 3) *reinterpret_cast<float2*>(R + (16 * r + i) * kLdT + 16 * c + j) = make_float2(x0, x1);
+        put_parts<3>(T + tri_block(r, c) * 256 + tri_at(i, j), kTri, x0, x1);
+      }
   }
-  __syncthreads();
-#pragma unroll
-  for (int c = 0; c < 4 - D; ++c) {
-    const int r = c + D;
-    float y = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(R + (16 * r + i) * kLdT + 16 * r + m);
-      y = fmaf(-x.x, E[c * 256 + m * 16 + j], y);
-      y = fmaf(-x.y, E[c * 256 + (m + 1) * 16 + j], y);
-      y = fmaf(-x.z, E[c * 256 + (m + 2) * 16 + j], y);
-      y = fmaf(-x.w, E[c * 256 + (m + 3) * 16 + j], y);
-    }
-    R[(16 * r + i) * kLdT + 16 * c + j] = y;
-  }
-  __syncthreads();
+  if (D < 3) __syncthreads();
 }
 
 // PP: parts of P that are stored
@@ -248,11 +256,12 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
       if (lane >= o) sum += y;
     }
     const double G0 = sum - x[1], G1 = sum, last = __shfl_sync(0xffffffffu, sum, 31);
-    s.G[2 * lane] = G0;
-    s.G[2 * lane + 1] = G1;
+    const float2 two[2] = {halves(G0), halves(G1)};
+    s.G[2 * lane] = two[0];
+    s.G[2 * lane + 1] = two[1];
     s.beta[2 * lane] = be[0];
     s.beta[2 * lane + 1] = be[1];
-    *reinterpret_cast<double2*>(a.G + at * kC + 2 * lane) = make_double2(G0, G1);
+    *reinterpret_cast<float4*>(a.G + at * kC + 2 * lane) = make_float4(two[0].x, two[0].y, two[1].x, two[1].y);
     float* v = a.vec + at * kVec;
     *reinterpret_cast<float2*>(v + 2 * lane) = make_float2(expf((float)G0), expf((float)G1));
     *reinterpret_cast<float2*>(v + 64 + 2 * lane) = make_float2(expf((float)(last - G0)), expf((float)(last - G1)));
@@ -283,7 +292,7 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool in = is_q ? i >= j + e : i > j + e;
-            x[e] = in ? acc[cb][t][2 * e2 + e] * expf((float)(s.G[i] - s.G[j + e])) * (is_q ? 1.f : s.beta[i]) : 0.f;
+            x[e] = acc[cb][t][2 * e2 + e] * decay(s.G[i], s.G[j + e], in) * (is_q ? 1.f : s.beta[i]);
           }
           if (is_q)
             put_parts<PP>(a.P + at * PP * kTri + tri_block(rb, cb) * 256 + tri_at(g + 8 * e2, 8 * t + c2), kTri, x[0], x[1]);
@@ -307,16 +316,17 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
     }
   }
   __syncthreads();
-  invert_level<1>(s.A, s.R, s.E, tid >> 4, tid & 15);
-  invert_level<2>(s.A, s.R, s.E, tid >> 4, tid & 15);
-  invert_level<3>(s.A, s.R, s.E, tid >> 4, tid & 15);
   bf16* T_out = a.T + at * 3 * kTri;
-  for (int i = tid; i < kTri / 2; i += 256) {
-    const int blk = i >> 7, e = (i & 127) * 2;
-    const int r = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, cb = blk - r * (r + 1) / 2;
-    const float2 x = *reinterpret_cast<const float2*>(s.R + (16 * r + (e >> 4)) * kLdT + 16 * cb + (e & 15));
-    put_parts<3>(T_out + blk * 256 + tri_at(e >> 4, e & 15), kTri, x.x, x.y);
+  {  // the diagonal blocks' parts
+    const int d = tid >> 6, i = (tid >> 2) & 15, j = (tid & 3) * 4;
+    const float4 x = *reinterpret_cast<const float4*>(s.R + (16 * d + i) * kLdT + 16 * d + j);
+    bf16* to = T_out + tri_block(d, d) * 256 + tri_at(i, j);
+    put_parts<3>(to, kTri, x.x, x.y);
+    put_parts<3>(to + 2, kTri, x.z, x.w);
   }
+  invert_level<1>(s.A, s.R, T_out, warp, lane);
+  invert_level<2>(s.A, s.R, T_out, warp, lane);
+  invert_level<3>(s.A, s.R, T_out, warp, lane);
 }
 
 // ------------------------------------------------------------------ state
@@ -819,7 +829,7 @@ template <typename T, int DK> struct GradSmem {
   float Tm[kC * kLdT];  // T, then M + M^T
   float P[kC * kLdT];   // P, then N = dP e^(G_i - G_j)
   float vec[kVec];
-  double G[kC];
+  float2 G[kC];
   float tok[kMaxWarps][3][kC];
   float rowP[kC], rowA[kC], rowB[kC];
   float col[kMaxWarps][kC];
@@ -1038,7 +1048,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
               const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
               const float x = acc[cb][t][e];
               if (is_a) {
-                const float dec = i > jj ? expf((float)(s.G[i] - s.G[jj])) : 0.f, be = s.vec[128 + i];
+                const float dec = decay(s.G[i], s.G[jj], i > jj), be = s.vec[128 + i];
                 const float ab = -x * dec * kk2[cb][t][e];
                 rowb[e >> 1] += ab;
                 row[e >> 1] += be * ab;
@@ -1050,7 +1060,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
                 const float dp = a.scale * x, y = i >= jj ? dp * s.P[i * kLdT + jj] : 0.f;
                 row[e >> 1] += y;
                 col[e & 1] += y;
-                s.P[i * kLdT + jj] = i >= jj ? dp * expf((float)(s.G[i] - s.G[jj])) : 0.f;
+                s.P[i * kLdT + jj] = dp * decay(s.G[i], s.G[jj], i >= jj);
               }
             }
 #pragma unroll
@@ -1196,7 +1206,7 @@ template <int DK> struct GradSmemB {
   bf16 P[3 * kTri];     // P, then N in the first two planes
   bf16 M[2 * kPlaneM];  // v [64][kLdG], then M + M^T
   float vec[kVec];
-  double G[kC];
+  float2 G[kC];
   float tok[8][3][kC];
   float rowP[10][16], colP[10][16], rowA[10][16], colA[10][16], rowB[10][16];
   float sdot[8];
@@ -1458,7 +1468,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               m[e] = acc[t][2 * r + e] + lo[t][2 * r + e];
-              dec[e] = (is_a ? i > j + e : i >= j + e) ? expf((float)(s.G[i] - s.G[j + e])) : 0.f;
+              dec[e] = decay(s.G[i], s.G[j + e], is_a ? i > j + e : i >= j + e);
             }
             if (is_a) {
               const float be = s.vec[128 + i];
