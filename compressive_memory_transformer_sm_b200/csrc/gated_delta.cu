@@ -87,9 +87,36 @@ int col_warps(int dv) { return (dv + 15) / 16; }
 
 int out_parts(int mode) { return (mode & INFINI_F32) ? 3 : 2; }
 
+// Microseconds of a pass with outputs of `strips` groups of 16 columns over n chunks, as measured (128 x 128 bf16): a
+// strip per SM 2.3 a chunk, two 3.8, four 5.3, and from there 9.2 per thousand strips.
+double pass_time(double strips, double n) {
+  return n * (strips <= kSms ? 2.3 : strips <= 2 * kSms ? 3.8 : std::max(5.3, 0.0092 * strips));
+}
+// Chunks per segment.  Segments run side by side, but all of them twice, and the first time with the unit vectors'
+// columns too: it pays where few (b, h) leave most SMs without work.  Measured at B 1, H 8, 512 chunks: forward 1174 us
+// in one piece, 820 in segments of 64; both passes of the backward, which fill the SMs better, 1403 and 1789.
+int segment_chunks(const Shape& s, long long chunks, bool bwd) {
+  const double strips = (double)s.B * s.H * col_warps(s.dv), unit = (double)s.B * s.H * padded_dk(s.dk) / 16;
+  const double whole = bwd ? 1.2 * pass_time(2 * strips, (double)chunks) : pass_time(strips, (double)chunks);
+  double best = 0.9 * whole;
+  long long seg = chunks;
+  for (long long n = 3; n <= 32 && chunks / n >= 4; ++n) {
+    const double each = (double)((chunks + n - 1) / n);
+    const double again = bwd ? 1.2 * pass_time(2 * n * strips, each) : pass_time(n * strips, each);
+    const double first = (bwd ? 1.2 : 0.9) * pass_time((n - 1) * (bwd ? 2 * strips + unit : strips + unit), each);
+    const double t = first + again + 5.5 * n + 10.;
+    if (t < best) {
+      best = t;
+      seg = (chunks + n - 1) / n;
+    }
+  }
+  return (int)seg;
+}
+
 // Workspace of nc chunks of every (b, h).
 struct ChunkSpace {
-  size_t T, P, vec, G, snap, dsnap, acc, bytes;
+  size_t T, P, vec, G, snap, dsnap, acc, segS, segD, segA, bytes;
+  int seg;
   ChunkSpace(const Shape& s, long long nc, bool bwd) {
     const size_t n = (size_t)s.B * s.H * nc, state = (size_t)col_warps(s.dv) * padded_dk(s.dk) * 16 * 4;
     size_t at = 0;
@@ -105,6 +132,11 @@ struct ChunkSpace {
     snap = take(bwd ? n * state : 0);
     dsnap = take(bwd ? n * state : 0);
     acc = take(bwd && s.H > s.Hk ? (size_t)s.B * s.Hk * nc * 2 * kC * padded_dk(s.dk) * 4 : 0);
+    seg = segment_chunks(s, nc, bwd);
+    const size_t nseg = (nc + seg - 1) / seg, m = nseg > 1 ? (size_t)s.B * s.H * nseg : 0;
+    segS = take(m * state);
+    segD = take(bwd ? m * state : 0);
+    segA = take(m * padded_dk(s.dk) * padded_dk(s.dk) * 4);
     bytes = at;
   }
   void place(ChunkArgs& a, void* ws) const {
@@ -116,6 +148,10 @@ struct ChunkSpace {
     a.snap = reinterpret_cast<float4*>(w + snap);
     a.dsnap = reinterpret_cast<float4*>(w + dsnap);
     a.acc = reinterpret_cast<float*>(w + acc);
+    a.segS = reinterpret_cast<float4*>(w + segS);
+    a.segD = reinterpret_cast<float4*>(w + segD);
+    a.segA = reinterpret_cast<float4*>(w + segA);
+    a.seg = seg;
   }
 };
 
@@ -172,37 +208,61 @@ template <typename T, int DK, int PP> StatePlan state_plan(int nw, long long hea
   return p;
 }
 
+void take_plan(ChunkArgs& a, const StatePlan& p) {
+  a.groups = p.groups;
+  a.stages = p.stages;
+  a.blocks = p.blocks;
+  a.first_loader = p.first_loader;
+}
+
 template <typename T, int DK, int PP> int run_prep(const ChunkArgs& a, cudaStream_t st) {
   return GD_LAUNCH((prep_kernel<T, DK, PP>), dim3(a.nc, a.H, a.B), 256, sizeof(PrepSmem<T, DK>), kPhaseUpdate, a, st);
 }
+template <typename T, int DK, int MODE> int run_forward(ChunkArgs a, int segments, int strips, cudaStream_t st) {
+  const StatePlan p = state_plan<T, DK, Dims<T, DK>::kOut>(strips, (long long)a.B * a.H * segments);
+  take_plan(a, p);
+  const dim3 grid(p.blocks * segments, a.H, a.B);
+  return p.KS == 4 ? GD_LAUNCH((forward_kernel<T, DK, 4, MODE>), grid, p.threads, p.smem, kPhaseState, a, st)
+                   : GD_LAUNCH((forward_kernel<T, DK, 1, MODE>), grid, p.threads, p.smem, kPhaseState, a, st);
+}
+template <typename T, int DK, bool SEG> int run_both(ChunkArgs a, int strips, cudaStream_t st) {
+  const StatePlan p = state_plan<T, DK, 3>(strips, 2LL * a.B * a.H * a.nseg);
+  take_plan(a, p);
+  const dim3 grid(2 * p.blocks * a.nseg, a.H, a.B);
+  return p.KS == 4 ? GD_LAUNCH((both_kernel<T, DK, 4, SEG>), grid, p.threads, p.smem, kPhaseBwd, a, st)
+                   : GD_LAUNCH((both_kernel<T, DK, 1, SEG>), grid, p.threads, p.smem, kPhaseBwd, a, st);
+}
+template <int DK> int run_combine(const ChunkArgs& a, int both, cudaStream_t st) {
+  if (a.nseg < 3) return INFINI_OK;
+  LaunchScope scope(kPhaseState, st);
+  combine_kernel<DK><<<dim3((1 + both) * col_warps(a.dv), a.H, a.B), 128, 0, st>>>(a, both);
+  return launch_status();
+}
 template <typename T, int DK> int chunk_forward(ChunkArgs a, long long chunks, long long slab, cudaStream_t st) {
-  constexpr int PP = Dims<T, DK>::kOut;
-  const StatePlan p = state_plan<T, DK, PP>(col_warps(a.dv), (long long)a.B * a.H);
-  a.groups = p.groups;
-  a.stages = p.stages;
-  a.first_loader = p.first_loader;
-  const dim3 grid(p.blocks, a.H, a.B);
+  const int nw = col_warps(a.dv);
   for (long long c = 0; c < chunks; c += slab) {
     a.c0 = (int)c;
     a.nc = (int)std::min(slab, chunks - c);
-    int rc = run_prep<T, DK, PP>(a, st);
-    if (rc == INFINI_OK)
-      rc = p.KS == 4 ? GD_LAUNCH((forward_kernel<T, DK, 4>), grid, p.threads, p.smem, kPhaseState, a, st)
-                     : GD_LAUNCH((forward_kernel<T, DK, 1>), grid, p.threads, p.smem, kPhaseState, a, st);
+    a.nseg = (a.nc + a.seg - 1) / a.seg;
+    int rc = run_prep<T, DK, Dims<T, DK>::kOut>(a, st);
+    if (rc == INFINI_OK && a.nseg > 1) {
+      rc = run_forward<T, DK, kPassSeg>(a, a.nseg - 1, nw + DK / 16, st);
+      if (rc == INFINI_OK) rc = run_combine<DK>(a, 0, st);
+    }
+    if (rc == INFINI_OK) rc = run_forward<T, DK, kPassOut>(a, a.nseg, nw, st);
     if (rc != INFINI_OK) return rc;
   }
   return INFINI_OK;
 }
 template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
+  const int nw = col_warps(a.dv);
+  a.nseg = (a.nc + a.seg - 1) / a.seg;
   int rc = run_prep<T, DK, 3>(a, st);
-  if (rc != INFINI_OK) return rc;
-  const StatePlan p = state_plan<T, DK, 3>(col_warps(a.dv), 2LL * a.B * a.H);
-  a.groups = p.groups;
-  a.stages = p.stages;
-  a.first_loader = p.first_loader;
-  const dim3 grid(2 * p.blocks, a.H, a.B);
-  rc = p.KS == 4 ? GD_LAUNCH((both_kernel<T, DK, 4>), grid, p.threads, p.smem, kPhaseBwd, a, st)
-                 : GD_LAUNCH((both_kernel<T, DK, 1>), grid, p.threads, p.smem, kPhaseBwd, a, st);
+  if (rc == INFINI_OK && a.nseg > 1) {
+    rc = run_both<T, DK, true>(a, nw + DK / 16, st);
+    if (rc == INFINI_OK) rc = run_combine<DK>(a, 1, st);
+  }
+  if (rc == INFINI_OK) rc = run_both<T, DK, false>(a, nw, st);
   if (rc != INFINI_OK) return rc;
   const dim3 chunks(a.nc, a.Hk, a.B);
   if constexpr (sizeof(T) == 2)

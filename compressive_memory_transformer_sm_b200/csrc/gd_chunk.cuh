@@ -62,6 +62,7 @@ struct ChunkArgs {
   // chunks c0 .. c0 + nc - 1 of every row are worked on; workspaces hold those
   int c0, nc;
   int groups;  // state kernels: groups of 16 value columns per block (a power of 2)
+  int blocks;  // ... blocks per (b, h) and segment
   int stages;  // ... chunks in shared memory, 1 or 2
   int first_loader;  // ... the threads from this one on copy the next chunk
   bf16* T;       // [B H][nc][3][kTri]: the three bf16 parts
@@ -70,7 +71,12 @@ struct ChunkArgs {
   float2* G;     // [B H][nc][64]: high and low part
   float4* snap;  // [B H][nc][nw][DK / 8][32]: states before the chunks (accumulator order)
   float4* dsnap; // the same of the gradients of the states after them
-  float* S;      // state_kernel: [B, H, dk, dv] read and written; grad: unused
+  // With few (b, h) a row's chunks are split into nseg segments of seg chunks that run side by side
+  int seg, nseg;
+  float4* segS;  // [B H][nseg][nw][DK / 8][32]: the state before a segment
+  float4* segD;  // [B H][nseg][nw][DK / 8][32]: the gradient of the state after it
+  float4* segA;  // [B H][nseg][DK / 16][DK / 8][32]: A with S_after = A S_before + B, 16 columns of it per strip
+  float* S;      // forward: [B, H, dk, dv], read and written
   void* out;
   const float* S0;  // bwd: initial values, may be null (zero)
   const float* dS;  // bwd: gradient of the final state, may be null
@@ -396,6 +402,13 @@ template <int N> __device__ __forceinline__ void state_store(const float (&S)[N]
       if (r < dk && x < dv) p[(long long)r * dv + x] = S[n][e];
     }
 }
+template <int N> __device__ __forceinline__ void state_get(float (&S)[N][4], const float4* p) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const float4 x = p[n * 32];
+    S[n][0] = x.x; S[n][1] = x.y; S[n][2] = x.z; S[n][3] = x.w;
+  }
+}
 template <int N> __device__ __forceinline__ void state_snap(const float (&S)[N][4], float4* p) {
 #pragma unroll
   for (int n = 0; n < N; ++n) p[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
@@ -409,23 +422,33 @@ template <int KS> __device__ __forceinline__ void group_sync(int group) {
     __syncwarp();
 }
 
-// One block: `groups` x 16 value columns of one (b, h), over all its chunks.  OUT: outputs are
-// computed and the final state goes back to S; otherwise the states before the chunks go to snap.
-template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int h, int b) {
+// What a pass over the chunks of a segment leaves behind.
+enum Pass {
+  kPassOut,   // outputs, and S after the row's last chunk
+  kPassSnap,  // the states before the chunks, for the gradients
+  kPassSeg    // segS: the state after the segment, from S where it is the first and from 0 in the others; segA:
+              // what the segment makes of each unit vector (value columns past nw: v = 0, S = I)
+};
+
+// One block: `groups` x 16 value columns of one segment of one (b, h).
+template <typename T, int DK, int KS, int MODE, int PP>
+__device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int seg, int h, int b) {
+  constexpr bool OUT = MODE == kPassOut;
   constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut;
   constexpr int NB = 4 / KS, ND = DK / KS / 8;  // token blocks and state tiles of a warp
   typedef Stage<T, DK, PP> St;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, c2 = 2 * (lane & 3);
   const int group = warp / KS, ks = warp % KS, ldv = strip_ld<T>(a.groups), nw = (a.dv + 15) >> 4;
-  const int wg = group < a.groups ? vblock * a.groups + group : nw;  // 16 columns from v0
+  const int wg = vblock * a.groups + group;  // 16 columns from v0
   const int v0 = 16 * wg, vb = 16 * vblock * a.groups, vs = 16 * group;
   const int hk = h / a.group;
   const size_t stage = stage_bytes<T, DK, PP>(a.groups);
   Exchange<DK, PO>& ex = reinterpret_cast<Exchange<DK, PO>*>(smem_raw + a.stages * stage)[KS > 1 ? group : 0];
   const long long len = row_len(a, b), bh = (long long)b * a.H + h;
-  const int nc = (int)min((long long)a.nc, max(0LL, (len + kC - 1) / kC - a.c0));
-  if (nc == 0) return;
+  const int all = (int)min((long long)a.nc, max(0LL, (len + kC - 1) / kC - a.c0));  // the row's chunks
+  const int first = seg * a.seg, nc = min(a.seg, all - first);
+  if (nc <= 0 || (MODE == kPassSeg && first + nc == all)) return;  // nothing follows a row's last segment
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1];
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
   const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[1] + vb;
@@ -433,19 +456,34 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
   const int w_in = min(16 * a.groups, a.dv - vb);
   auto fetch = [&](int i) {
     if (tid < a.first_loader) return;
-    const long long t0 = ((long long)a.c0 + i) * kC, at = bh * a.nc + i;
+    const long long t0 = ((long long)a.c0 + first + i) * kC, at = bh * a.nc + first + i;
     const Fetch f = {k + t0 * a.ks[2], OUT ? q + t0 * a.qs[2] : nullptr, v + t0 * a.vs[2], a.ks[2], a.qs[2], a.vs[2],
-                     chunk_len(len, a.c0 + i), a.dk, w_in, a.vec_k, a.vec_v, a.T + at * 3 * kTri,
+                     chunk_len(len, (long long)a.c0 + first + i), a.dk, w_in, a.vec_k, a.vec_v, a.T + at * 3 * kTri,
                      OUT ? a.P + at * PP * kTri : nullptr, a.vec + at * kVec};
     fetch_chunk<T, DK, PP>(*reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage), f, ldv, 16 * a.groups,
                            tid - a.first_loader, nthr - a.first_loader);
   };
-  const bool live = wg < nw;
+  const bool unit = MODE == kPassSeg && wg >= nw;  // columns of the identity
+  const bool live = group < a.groups && wg < nw + (MODE == kPassSeg && seg > 0 ? DK / 16 : 0);
   // a warp's tiles of 8 tokens: all of them (KS 1), or tiles ks and 7 - ks, so that the triangular products balance
   auto tile = [&](int x, int y) { return KS == 1 ? 2 * x + y : y ? 7 - ks : ks; };
   float S[ND][4];
-  const float* from = OUT ? a.S : a.S0;
-  state_load<ND>(S, from ? from + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
+  float4* before = a.segS + (((bh * a.nseg + seg) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane;
+  if (MODE != kPassSeg && a.nseg > 1 && nc < all) {
+    if (live) state_get<ND>(S, before);
+  } else {
+    const float* from = MODE == kPassSeg && seg > 0 ? nullptr : a.S ? a.S : a.S0;
+    state_load<ND>(S, from ? from + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
+    if (unit) {
+#pragma unroll
+      for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[n][e] = ks * DK / KS + 8 * n + c2 + (e & 1) == 16 * (wg - nw) + (lane >> 2) + 8 * (e >> 1) ? 1.f : 0.f;
+    } else if (MODE == kPassSeg && seg == 0 && live) {
+      state_snap<ND>(S, before);
+    }
+  }
   fetch(0);
   for (int i = 0; i < nc; ++i) {
     if constexpr (KS > 1)
@@ -460,7 +498,7 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
     T* sv = reinterpret_cast<T*>(&s + 1);
     auto vec2 = [&](int which, int t) { return *reinterpret_cast<const float2*>(s.vec + 64 * which + 8 * t + c2); };
     if (live) {
-      if (!OUT) state_snap<ND>(S, a.snap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
+      if (MODE == kPassSnap) state_snap<ND>(S, a.snap + (((bh * a.nc + first + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // R^T = S^T K^T, Y^T = S^T Q^T
       float R[NB][2][4] = {}, Y[NB][2][4] = {}, lo[NB][2][4] = {};
 #pragma unroll
@@ -588,8 +626,8 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
             for (int x = kk; x < NB; ++x) mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, x, kk, lane));
         }
         __syncwarp();  // every lane has taken its v
-        const int n = chunk_len(len, a.c0 + i), w = min(16, a.dv - v0);
-        T* o = out + ((long long)a.c0 + i) * kC * a.os[2] + vs;
+        const int n = chunk_len(len, (long long)a.c0 + first + i), w = min(16, a.dv - v0);
+        T* o = out + ((long long)a.c0 + first + i) * kC * a.os[2] + vs;
 #pragma unroll
         for (int x = 0; x < NB; ++x)
 #pragma unroll
@@ -633,40 +671,56 @@ template <typename T, int DK, int KS, bool OUT, int PP> __device__ __forceinline
       if (i + 1 < nc) fetch(i + 1);
     }
   }
-  if (OUT && live) state_store<ND>(S, a.S + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
+  if (OUT && live && first + nc == all) state_store<ND>(S, a.S + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
+  if (MODE == kPassSeg && live) {
+    if (unit)
+      state_snap<ND>(S, a.segA + (((bh * a.nseg + seg) * (DK / 16) + wg - nw) * (DK / 8) + ks * ND) * 32 + lane);
+    else if (seg + 1 < a.nseg)
+      state_snap<ND>(S, before + (long long)nw * (DK / 8) * 32);
+  }
 }
 
-// The gradient of the state from the last chunk to the first.
-template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_pass(const ChunkArgs& a, int vblock, int h, int b) {
+// The gradient of the state from a segment's last chunk to its first.  SEG: from dS where it is the
+// row's last and from 0 in the others, to segD of the segment before.
+template <typename T, int DK, int KS, bool SEG>
+__device__ __forceinline__ void bwd_state_pass(const ChunkArgs& a, int vblock, int seg, int h, int b) {
   constexpr int LD = Dims<T, DK>::kLdK, PI = Dims<T, DK>::kIn, PO = Dims<T, DK>::kOut;
   constexpr int NB = 4 / KS, ND = DK / KS / 8;
   typedef Stage<T, DK, 3> St;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, c2 = 2 * (lane & 3);
   const int group = warp / KS, ks = warp % KS, ldv = strip_ld<T>(a.groups), nw = (a.dv + 15) >> 4;
-  const int wg = group < a.groups ? vblock * a.groups + group : nw;
+  const int wg = vblock * a.groups + group;
   const int v0 = 16 * wg, vb = 16 * vblock * a.groups, vs = 16 * group;
   const int hk = h / a.group;
   const size_t stage = stage_bytes<T, DK, 3>(a.groups);
   Exchange<DK, PO>& ex = reinterpret_cast<Exchange<DK, PO>*>(smem_raw + a.stages * stage)[KS > 1 ? group : 0];
   const long long len = row_len(a, b), bh = (long long)b * a.H + h;
-  const int nc = (int)min((long long)a.nc, (len + kC - 1) / kC);
+  const int all = (int)min((long long)a.nc, (len + kC - 1) / kC);  // the row's chunks
+  const int first = seg * a.seg, nc = min(a.seg, all - first);
+  if (SEG ? nc <= 0 || seg == 0 : nc <= 0 && seg > 0) return;
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1];
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1];
   const T* d_out = static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + vb;
   const int w_in = min(16 * a.groups, a.dv - vb);
   auto fetch = [&](int i) {
     if (tid < a.first_loader) return;
-    const long long t0 = (long long)i * kC, at = bh * a.nc + i;
-    const Fetch f = {k + t0 * a.ks[2], q + t0 * a.qs[2], d_out + t0 * a.os[2], a.ks[2], a.qs[2], a.os[2], chunk_len(len, i),
+    const long long t0 = (long long)(first + i) * kC, at = bh * a.nc + first + i;
+    const Fetch f = {k + t0 * a.ks[2], q + t0 * a.qs[2], d_out + t0 * a.os[2], a.ks[2], a.qs[2], a.os[2], chunk_len(len, first + i),
                      a.dk, w_in, a.vec_k, a.vec_o, a.T + at * 3 * kTri, a.P + at * 3 * kTri, a.vec + at * kVec};
     fetch_chunk<T, DK, 3>(*reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage), f, ldv, 16 * a.groups,
                           tid - a.first_loader, nthr - a.first_loader);
   };
-  const bool live = wg < nw;
+  const bool live = group < a.groups && wg < nw;
   auto tile = [&](int x, int y) { return KS == 1 ? 2 * x + y : y ? 7 - ks : ks; };
   float S[ND][4];
-  state_load<ND>(S, a.dS ? a.dS + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
+  const bool last = first + nc >= all;
+  float4* after = a.segD + (((bh * a.nseg + seg) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane;
+  if (!SEG && !last) {
+    if (live) state_get<ND>(S, after);
+  } else {
+    state_load<ND>(S, a.dS && last ? a.dS + bh * a.dk * a.dv : nullptr, ks * DK / KS, v0, a.dk, a.dv, lane);
+  }
   if (nc > 0) fetch(nc - 1);
   for (int i = nc - 1; i >= 0; --i) {
     if constexpr (KS > 1)
@@ -681,7 +735,7 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
     const T* sd = reinterpret_cast<const T*>(&s + 1);
     auto vec2 = [&](int which, int t) { return *reinterpret_cast<const float2*>(s.vec + 64 * which + 8 * t + c2); };
     if (live) {
-      state_snap<ND>(S, a.dsnap + (((bh * a.nc + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
+      if (!SEG) state_snap<ND>(S, a.dsnap + (((bh * a.nc + first + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // dU^T = scale dO^T P + rho (dS^T K^T)
       float U[NB][2][4] = {}, W[NB][2][4] = {}, lo[NB][2][4] = {}, lw[NB][2][4] = {};
 #pragma unroll
@@ -800,22 +854,79 @@ template <typename T, int DK, int KS> __device__ __forceinline__ void bwd_state_
       if (i > 0) fetch(i - 1);
     }
   }
-  if (a.dS0 && live) state_store<ND>(S, a.dS0 + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
+  if (SEG && live) state_snap<ND>(S, after - (long long)nw * (DK / 8) * 32);
+  if (!SEG && a.dS0 && seg == 0 && live) state_store<ND>(S, a.dS0 + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
 }
 
 // Threads at most: two (KS 4) or four (KS 1) groups and four copying warps.
 constexpr int state_threads(int KS) { return KS == 4 ? 384 : 256; }
 
-template <typename T, int DK, int KS> __global__ void __launch_bounds__(state_threads(KS)) forward_kernel(const ChunkArgs a) {
-  state_pass<T, DK, KS, true, Dims<T, DK>::kOut>(a, blockIdx.x, blockIdx.y, blockIdx.z);
+// Blocks: gridDim.x = segments x blocks per segment.
+template <typename T, int DK, int KS, int MODE> __global__ void __launch_bounds__(state_threads(KS)) forward_kernel(const ChunkArgs a) {
+  state_pass<T, DK, KS, MODE, Dims<T, DK>::kOut>(a, blockIdx.x % a.blocks, blockIdx.x / a.blocks, blockIdx.y, blockIdx.z);
 }
 // The two passes of the backward do not depend on each other: even blocks run the states forward,
 // odd ones their gradients backward.
-template <typename T, int DK, int KS> __global__ void __launch_bounds__(state_threads(KS)) both_kernel(const ChunkArgs a) {
+template <typename T, int DK, int KS, bool SEG> __global__ void __launch_bounds__(state_threads(KS)) both_kernel(const ChunkArgs a) {
+  const int x = blockIdx.x >> 1;
   if (blockIdx.x & 1)
-    bwd_state_pass<T, DK, KS>(a, blockIdx.x >> 1, blockIdx.y, blockIdx.z);
+    bwd_state_pass<T, DK, KS, SEG>(a, x % a.blocks, x / a.blocks, blockIdx.y, blockIdx.z);
   else
-    state_pass<T, DK, KS, false, 3>(a, blockIdx.x >> 1, blockIdx.y, blockIdx.z);
+    state_pass<T, DK, KS, SEG ? kPassSeg : kPassSnap, 3>(a, x % a.blocks, x / a.blocks, blockIdx.y, blockIdx.z);
+}
+
+// The states between segments from what each makes of a zero state (in segS, segD) and of the unit
+// vectors: S_(i+1) = A_i S_i + B_i; odd blocks (backward): D_(i-1) = A_i^T D_i + C_i.  A block: 16
+// value columns of one (b, h), four warps with DK / 4 key rows each.
+template <int DK> __global__ void __launch_bounds__(128) combine_kernel(const ChunkArgs a, int both) {
+  constexpr int ND = DK / 32, NS = DK / 16;
+  __shared__ uint4 ex[NS][3][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = (a.dv + 15) >> 4;
+  const bool back = both && (blockIdx.x & 1);
+  const int wg = both ? blockIdx.x >> 1 : blockIdx.x;
+  const long long bh = (long long)blockIdx.z * a.H + blockIdx.y, len = row_len(a, blockIdx.z);
+  const int all = (int)min((long long)a.nc, max(0LL, (len + kC - 1) / kC - a.c0)), n = (all + a.seg - 1) / a.seg;  // live segments
+  if (n < 3) return;
+  const long long step = (long long)nw * (DK / 8) * 32;
+  float4* at = (back ? a.segD : a.segS) + ((bh * a.nseg * nw + wg) * (DK / 8) + warp * ND) * 32 + lane;
+  const float4* A = a.segA + bh * a.nseg * NS * (DK / 8) * 32 + lane;
+  float S[ND][4];
+  state_get<ND>(S, at + (back ? n - 2 : 1) * step);
+  for (int k = 1; k < n - 1; ++k) {
+    const int i = back ? n - 1 - k : k;  // the segment that is passed
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < ND / 2; ++x) put_frag<3>(ex[warp * (ND / 2) + x][0], from_acc<3>(S[2 * x], S[2 * x + 1]), lane);
+    __syncthreads();
+    const float4* Ai = A + (long long)i * NS * (DK / 8) * 32;
+    float4* to = at + (back ? i - 1 : i + 1) * step;
+    float hi[ND][4], lo[ND][4] = {};
+    state_get<ND>(hi, to);
+#pragma unroll 2
+    for (int kk = 0; kk < NS; ++kk) {
+      const AFrag<3> f = get_frag<3>(ex[kk][0], lane);
+#pragma unroll
+      for (int x = 0; x < ND / 2; ++x) {
+        const int np = warp * (ND / 2) + x;
+        BFrag<3> m;
+        if (!back) {  // B[k = column of A][n = its row]
+          m = b_from_acc<3>(Ai[(kk * (DK / 8) + 2 * np) * 32], Ai[(kk * (DK / 8) + 2 * np + 1) * 32]);
+        } else {  // B[k = row of A][n = its column]
+          const float4 t0 = Ai[(np * (DK / 8) + 2 * kk) * 32], t1 = Ai[(np * (DK / 8) + 2 * kk + 1) * 32];
+          split<3>(t0.x, t0.y, m.r, 0);
+          split<3>(t1.x, t1.y, m.r, 1);
+          split<3>(t0.z, t0.w, m.r, 2);
+          split<3>(t1.z, t1.w, m.r, 3);
+        }
+        mma2(hi[2 * x], hi[2 * x + 1], lo[2 * x], lo[2 * x + 1], f, m);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < ND; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[x][e] = hi[x][e] + lo[x][e];
+    state_snap<ND>(S, to);
+  }
 }
 
 // ------------------------------------------------------------------ gradients

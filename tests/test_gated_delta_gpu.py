@@ -367,3 +367,17 @@ def test_norm_memory_and_gradients_together():
     near(dx, wx)
     near(dw, ww)
     near(db, wb)
+
+
+@pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,Hk,L,dk,dv,lens", [(1, 1, 1, 2500, 128, 128, None), (3, 1, 1, 2100, 64, 40, [2100, 0, 700]),
+                                                (2, 2, 1, 1700, 33, 128, [1, 1700])])
+def test_long_sequences_of_few_heads(B, H, Hk, L, dk, dv, lens, t):
+    """Long enough, with few (b, h), for the sequence to be cut into segments that run side by side."""
+    x, d_out, dS = backward_inputs(B, H, Hk, L, dk, dv, t, seed=6)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    check_forward(*x, *forward(*x, lens=ln), lens=ln)
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS, lens=ln)
+    check_backward(x, d_out, dS, got, lens=ln)
+    got2 = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS, lens=ln)
+    assert all(torch.equal(a, b) for a, b in zip(got, got2))
