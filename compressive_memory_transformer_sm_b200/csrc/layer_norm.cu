@@ -35,6 +35,29 @@ template <> struct Raw<float, 1> { float u; };
 template <int VEC, typename T> __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
   return *reinterpret_cast<const Raw<T, VEC>*>(p);
 }
+// Elements lo .. hi - 1 of a vector, zeros around them (kept in registers: no array is indexed).
+template <int VEC> __device__ __forceinline__ Raw<__nv_bfloat16, VEC> load_edge(const __nv_bfloat16* p, int lo, int hi) {
+  const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    uint32_t x = 0;
+    if (i >= lo && i < hi) x = u[i];
+    w[i / 2] |= x << (16 * (i % 2));
+  }
+  Raw<__nv_bfloat16, VEC> r;
+  r.u = make_uint4(w[0], w[1], w[2], w[3]);
+  return r;
+}
+template <int VEC> __device__ __forceinline__ Raw<float, VEC> load_edge(const float* p, int lo, int hi) {
+  float x[4] = {};
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+    if (i >= lo && i < hi) x[i] = p[i];
+  Raw<float, VEC> r;
+  r.u = make_float4(x[0], x[1], x[2], x[3]);
+  return r;
+}
 template <typename T, int VEC> __device__ __forceinline__ Floats<VEC> floats(const Raw<T, VEC>& r) {
   Floats<VEC> f;
   if constexpr (VEC == 8) {
@@ -121,6 +144,7 @@ template <int TPR, int N> __device__ __forceinline__ void row_sum(float (&x)[N],
   }
 }
 
+
 struct Args {
   const void* x;
   const void* weight;
@@ -132,6 +156,7 @@ struct Args {
   int D;
   float eps;
   bool w32;       // weight and bias are fp32
+  int shift;      // elements by which x, dy and y lie behind a multiple of 16 bytes
   bool has_bias;  // backward: dbias is wanted
 };
 
@@ -141,37 +166,69 @@ template <int TPR> constexpr int kBlockThreads = TPR < 128 ? 128 : TPR;
 // (Re-read for each row they cost four times the row itself from L2: 146 us at 32768 x 4096 bf16.)
 constexpr int kKeep = 16;
 
-// A thread's part of row `row`; zeros behind the row's end.
-template <typename T, int VEC, int TPR, int NV>
-__device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* x, long long row, bool active, int lane, int D) {
-  const T* p = static_cast<const T*>(x) + row * D;
+// Column of element 0 of a thread's vector v.  SHIFT: rows do not start on 16 bytes; a row's vectors
+// then are those of memory, the first starting `off` elements before the row, so that all but the
+// first and the last are still loaded and stored whole.  A thread's rows are a multiple of VEC
+// apart: off, and with it the columns it holds, is the same for all of them.
+template <int VEC, int TPR> __device__ __forceinline__ int column(int v, int lane, int off) { return (v * TPR + lane) * VEC - off; }
+
+// A thread's part of row `row`.  SHIFT: a row's first and last vector hold elements of its neighbours too, which
+// inside() leaves out where they are used; only at the tensor's own ends are elements loaded one by one (putting a
+// vector together there waits for its loads, and with it the whole prefetch).
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
+__device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* x, long long row, const Args& a, int lane, int off) {
+  const T* p = static_cast<const T*>(x) + row * a.D;
+  const bool active = row < a.rows;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int at = (v * TPR + lane) * VEC;
+    const int at = column<VEC, TPR>(v, lane, off);
     r[v] = Raw<T, VEC>{};
-    if (active && at < D) r[v] = load_raw<VEC>(p + at);
+    if (!active || at >= a.D) continue;
+    if constexpr (SHIFT)
+      if ((row == 0 && at < 0) || (row == a.rows - 1 && at + VEC > a.D)) {
+        r[v] = load_edge<VEC>(p + at, -at, a.D - at);
+        continue;
+      }
+    r[v] = load_raw<VEC>(p + at);
   }
 }
-template <int VEC, int TPR, int NV>
-__device__ __forceinline__ void load_weights(Floats<VEC> (&w)[NV], const void* p, bool f32, int lane, int D) {
+template <bool SHIFT> __device__ __forceinline__ bool inside(int at, int e, int D) { return SHIFT ? at + e >= 0 && at + e < D : at < D; }
+template <int VEC, int TPR, bool SHIFT, typename T> __device__ __forceinline__ void store_part(T* p, int at, int D, const Floats<VEC>& o) {
+  if constexpr (SHIFT) {
+    if (at >= 0 && at + VEC <= D) {
+      store_vec<VEC>(p + at, o);
+    } else {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int at = (v * TPR + lane) * VEC;
-    w[v] = {};
-    if (p && at < D) w[v] = load_weight<VEC>(p, f32, at);
+      for (int i = 0; i < VEC; ++i)
+        if (at + i >= 0 && at + i < D) p[at + i] = from_f32<T>(o.v[i]);
+    }
+  } else {
+    store_vec<VEC>(p + at, o);
   }
 }
-// xs: the row's elements less their mean, 0 behind its end; returns the variance.
-template <typename T, int VEC, int TPR, int NV>
-__device__ __forceinline__ float centre(const Raw<T, VEC> (&r)[NV], int lane, int D, float (&xs)[NV][VEC], float* red, int sub, int red_stride) {
+template <int VEC, bool SHIFT> __device__ __forceinline__ Floats<VEC> weight_part(const void* p, bool f32, int at, int D) {
+  Floats<VEC> w = {};
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (at + i >= 0 && at + i < D) w.v[i] = f32 ? static_cast<const float*>(p)[at + i] : to_f32(static_cast<const __nv_bfloat16*>(p)[at + i]);
+  } else {
+    if (at < D) w = load_weight<VEC>(p, f32, at);
+  }
+  return w;
+}
+// xs: the row's elements less their mean, 0 outside the row; returns the variance.
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
+__device__ __forceinline__ float centre(const Raw<T, VEC> (&r)[NV], int lane, int D, int off, float (&xs)[NV][VEC], float* red, int sub, int red_stride) {
   float s[1] = {0.f};
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const Floats<VEC> f = floats(r[v]);
+    const int at = column<VEC, TPR>(v, lane, off);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      xs[v][e] = f.v[e];
-      s[0] += f.v[e];
+      xs[v][e] = !SHIFT || inside<SHIFT>(at, e, D) ? f.v[e] : 0.f;
+      s[0] += xs[v][e];
     }
   }
   row_sum<TPR>(s, red, sub);
@@ -179,10 +236,10 @@ __device__ __forceinline__ float centre(const Raw<T, VEC> (&r)[NV], int lane, in
   float q[1] = {0.f};
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const bool in = (v * TPR + lane) * VEC < D;
+    const int at = column<VEC, TPR>(v, lane, off);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      xs[v][e] = in ? xs[v][e] - mean : 0.f;
+      xs[v][e] = inside<SHIFT>(at, e, D) ? xs[v][e] - mean : 0.f;
       q[0] = fmaf(xs[v][e], xs[v][e], q[0]);
     }
   }
@@ -190,7 +247,7 @@ __device__ __forceinline__ float centre(const Raw<T, VEC> (&r)[NV], int lane, in
   return q[0] / (float)D;
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_forward_kernel(const Args a) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR, NW = TPR > 32 ? TPR / 32 : 1;
   constexpr bool KEEP = NV * VEC <= kKeep;
@@ -198,58 +255,65 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_forward_kernel(const Ar
   const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + sub;
+  const int off = SHIFT ? (int)((a.shift + row * a.D) % VEC) : 0;
   Raw<T, VEC> next[NV];
-  load_row<T, VEC, TPR, NV>(next, a.x, row, row < a.rows, lane, a.D);
+  load_row<T, VEC, TPR, NV, SHIFT>(next, a.x, row, a, lane, off);
   Floats<VEC> w[KEEP ? NV : 1], b[KEEP ? NV : 1];
-  if constexpr (KEEP) {
-    load_weights<VEC, TPR, NV>(w, a.weight, a.w32, lane, a.D);
-    load_weights<VEC, TPR, NV>(b, a.bias, a.w32, lane, a.D);
-  }
+  if constexpr (KEEP)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = column<VEC, TPR>(v, lane, off);
+      w[v] = weight_part<VEC, SHIFT>(a.weight, a.w32, at, a.D);
+      b[v] = {};
+      if (a.bias) b[v] = weight_part<VEC, SHIFT>(a.bias, a.w32, at, a.D);
+    }
   for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
     Raw<T, VEC> cur[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) cur[v] = next[v];
-    load_row<T, VEC, TPR, NV>(next, a.x, row + step, row + step < a.rows, lane, a.D);
+    load_row<T, VEC, TPR, NV, SHIFT>(next, a.x, row + step, a, lane, off);
     float xs[NV][VEC];
-    const float var = centre<T, VEC, TPR, NV>(cur, lane, a.D, xs, red, sub, RPB * NW);
+    const float var = centre<T, VEC, TPR, NV, SHIFT>(cur, lane, a.D, off, xs, red, sub, RPB * NW);
     const float rstd = 1.f / sqrtf(var + a.eps);
     if (!active) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int at = (v * TPR + lane) * VEC;
+      const int at = column<VEC, TPR>(v, lane, off);
       if (at < a.D) {
         Floats<VEC> wv, bv = {}, o;
         if constexpr (KEEP) {
           wv = w[v];
           bv = b[v];
         } else {
-          wv = load_weight<VEC>(a.weight, a.w32, at);
-          if (a.bias) bv = load_weight<VEC>(a.bias, a.w32, at);
+          wv = weight_part<VEC, SHIFT>(a.weight, a.w32, at, a.D);
+          if (a.bias) bv = weight_part<VEC, SHIFT>(a.bias, a.w32, at, a.D);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o.v[e] = fmaf(xs[v][e] * rstd, wv.v[e], bv.v[e]);
-        store_vec<VEC>(static_cast<T*>(a.y) + row * a.D + at, o);
+        store_part<VEC, TPR, SHIFT>(static_cast<T*>(a.y) + row * a.D, at, a.D, o);
       }
     }
   }
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const Args a) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR, NW = TPR > 32 ? TPR / 32 : 1, E = NV * VEC;
   constexpr bool KEEP = E <= kKeep;
-  // statistics of the two sums of a row, then (RPB > 1) the rows' accumulators of the block
-  __shared__ float red[4 * RPB * NW];
-  extern __shared__ float acc[];  // [RPB > 1 ? TPR * E * 2 : 0]
+  __shared__ float red[4 * RPB * NW];  // statistics, then the two sums of a row
+  extern __shared__ float acc[];       // RPB > 1: [2][D], the block's sums over its rows in flight
   const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + sub;
+  const int off = SHIFT ? (int)((a.shift + row * a.D) % VEC) : 0;
   Raw<T, VEC> nx[NV], nd[NV];
-  load_row<T, VEC, TPR, NV>(nx, a.x, row, row < a.rows, lane, a.D);
-  load_row<T, VEC, TPR, NV>(nd, a.dy, row, row < a.rows, lane, a.D);
+  load_row<T, VEC, TPR, NV, SHIFT>(nx, a.x, row, a, lane, off);
+  load_row<T, VEC, TPR, NV, SHIFT>(nd, a.dy, row, a, lane, off);
   Floats<VEC> w[KEEP ? NV : 1];
-  if constexpr (KEEP) load_weights<VEC, TPR, NV>(w, a.weight, a.w32, lane, a.D);
+  if constexpr (KEEP)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) w[v] = weight_part<VEC, SHIFT>(a.weight, a.w32, column<VEC, TPR>(v, lane, off), a.D);
   float dw[NV][VEC] = {}, db[NV][VEC] = {};
   for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
@@ -259,23 +323,23 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const A
       cx[v] = nx[v];
       cd[v] = nd[v];
     }
-    load_row<T, VEC, TPR, NV>(nx, a.x, row + step, row + step < a.rows, lane, a.D);
-    load_row<T, VEC, TPR, NV>(nd, a.dy, row + step, row + step < a.rows, lane, a.D);
+    load_row<T, VEC, TPR, NV, SHIFT>(nx, a.x, row + step, a, lane, off);
+    load_row<T, VEC, TPR, NV, SHIFT>(nd, a.dy, row + step, a, lane, off);
     float xs[NV][VEC];
-    const float var = centre<T, VEC, TPR, NV>(cx, lane, a.D, xs, red, sub, RPB * NW);
+    const float var = centre<T, VEC, TPR, NV, SHIFT>(cx, lane, a.D, off, xs, red, sub, RPB * NW);
     const float rstd = 1.f / sqrtf(var + a.eps);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int at = (v * TPR + lane) * VEC;
-      const Floats<VEC> d = floats(cd[v]);
-      Floats<VEC> wv = {};
+      const int at = column<VEC, TPR>(v, lane, off);
+      Floats<VEC> d = floats(cd[v]), wv;
       if constexpr (KEEP)
         wv = w[v];
-      else if (at < a.D)
-        wv = load_weight<VEC>(a.weight, a.w32, at);
+      else
+        wv = weight_part<VEC, SHIFT>(a.weight, a.w32, at, a.D);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
+        if (SHIFT && !inside<SHIFT>(at, e, a.D)) d.v[e] = 0.f;
         xs[v][e] *= rstd;
         dw[v][e] = fmaf(d.v[e], xs[v][e], dw[v][e]);
         db[v][e] += d.v[e];
@@ -289,56 +353,47 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const A
     if (active) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int at = (v * TPR + lane) * VEC;
+        const int at = column<VEC, TPR>(v, lane, off);
         if (at < a.D) {
           const Floats<VEC> d = floats(cd[v]);
           Floats<VEC> wv, o;
           if constexpr (KEEP)
             wv = w[v];
           else
-            wv = load_weight<VEC>(a.weight, a.w32, at);
+            wv = weight_part<VEC, SHIFT>(a.weight, a.w32, at, a.D);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) o.v[e] = rstd * (d.v[e] * wv.v[e] - m0 - xs[v][e] * m1);
-          store_vec<VEC>(static_cast<T*>(a.y) + row * a.D + at, o);
+          store_part<VEC, TPR, SHIFT>(static_cast<T*>(a.y) + row * a.D, at, a.D, o);
         }
       }
     }
   }
-  // the block's sum over its RPB rows in flight, in their order
-  if constexpr (RPB > 1) {
-    for (int r = RPB - 1; r > 0; --r) {
-      __syncthreads();
-      if (sub == r)
+  // the block's sum over its RPB rows in flight, in their order, column by column
+  float* pw = a.partial + (long long)blockIdx.x * 2 * a.D;
+  for (int r = 0; r < RPB; ++r) {
+    if (sub == r)
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            acc[(v * VEC + e) * TPR + lane] = dw[v][e];
-            acc[(E + v * VEC + e) * TPR + lane] = db[v][e];
+        for (int e = 0; e < VEC; ++e) {
+          const int at = column<VEC, TPR>(v, lane, off) + e;
+          if (at < 0 || at >= a.D) continue;
+          float x = dw[v][e], y = db[v][e];
+          if constexpr (RPB > 1) {
+            if (r > 0) {
+              x += acc[at];
+              y += acc[a.D + at];
+            }
+            if (r + 1 < RPB) {
+              acc[at] = x;
+              acc[a.D + at] = y;
+              continue;
+            }
           }
-      __syncthreads();
-      if (sub == r - 1)
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            dw[v][e] += acc[(v * VEC + e) * TPR + lane];
-            db[v][e] += acc[(E + v * VEC + e) * TPR + lane];
-          }
-    }
-  }
-  if (sub == 0) {
-    float* pw = a.partial + (long long)blockIdx.x * 2 * a.D;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int at = (v * TPR + lane) * VEC + e;
-        if (at < a.D) {
-          pw[at] = dw[v][e];
-          pw[a.D + at] = db[v][e];
+          pw[at] = x;
+          pw[a.D + at] = y;
         }
-      }
+    if constexpr (RPB > 1) __syncthreads();
   }
 }
 
@@ -379,48 +434,55 @@ template <typename F> int resident_blocks(F* kernel, int threads, size_t smem) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) == cudaSuccess && n > 0 ? n * kSms : kSms;
 }
 
-template <typename T, int VEC, int TPR, int NV> int launch(const Args& a, bool bwd, cudaStream_t st, int* parts) {
+// A multiple of VEC rows between a thread's rows (SHIFT).
+int whole_blocks(long long most, long long blocks, int rpb, int vec) {
+  if (most <= blocks) return (int)most;
+  const int unit = std::max(1, vec / rpb);
+  return (int)(blocks / unit * unit);
+}
+
+template <typename T, int VEC, int TPR, int NV, bool SHIFT> int launch(const Args& a, bool bwd, cudaStream_t st, int* parts) {
   constexpr int TH = kBlockThreads<TPR>, RPB = TH / TPR;
   const long long most = (a.rows + RPB - 1) / RPB;
   if (!bwd) {
-    static const int resident = resident_blocks(ln_forward_kernel<T, VEC, TPR, NV>, TH, 0);
+    static const int resident = resident_blocks(ln_forward_kernel<T, VEC, TPR, NV, SHIFT>, TH, 0);
     LaunchScope scope(kPhasePre, st);
-    ln_forward_kernel<T, VEC, TPR, NV><<<(int)std::min<long long>(most, resident), TH, 0, st>>>(a);
+    ln_forward_kernel<T, VEC, TPR, NV, SHIFT><<<whole_blocks(most, resident, RPB, VEC), TH, 0, st>>>(a);
   } else {
-    const size_t smem = RPB > 1 ? (size_t)TPR * NV * VEC * 2 * 4 : 0;
-    static const int resident = resident_blocks(ln_backward_kernel<T, VEC, TPR, NV>, TH, smem);
-    *parts = (int)std::min<long long>(backward_blocks(a.rows, RPB), resident);
+    const size_t smem = RPB > 1 ? (size_t)2 * a.D * 4 : 0;
+    static const int resident = resident_blocks(ln_backward_kernel<T, VEC, TPR, NV, SHIFT>, TH, RPB > 1 ? (size_t)2 * TPR * NV * VEC * 4 : 0);
+    *parts = whole_blocks(most, std::min<long long>(backward_blocks(a.rows, RPB), resident), RPB, VEC);
     LaunchScope scope(kPhaseBwd, st);
-    ln_backward_kernel<T, VEC, TPR, NV><<<*parts, TH, smem, st>>>(a);
+    ln_backward_kernel<T, VEC, TPR, NV, SHIFT><<<*parts, TH, smem, st>>>(a);
   }
   return launch_status();
 }
 
-// Threads per row and vectors per thread by the number of vectors of a row.  Scalars (VEC = 1)
-// where D is not a multiple of 16 bytes or a pointer is not aligned to them.
+// Threads per row and vectors per thread by the number of vectors of a row; a multiple of 16 bytes
+// to a row or (SHIFT) not.  VEC 1 where x, dy and y lie on different 16-byte grids.
+template <typename T, int V, bool SHIFT> int dispatch_rows(const Args& a, bool bwd, cudaStream_t st, int* parts) {
+  const int n = SHIFT ? (a.D + 2 * (V - 1)) / V : a.D / V;
+  if (n <= 8) return launch<T, V, 8, 1, SHIFT>(a, bwd, st, parts);
+  if (n <= 16) return launch<T, V, 16, 1, SHIFT>(a, bwd, st, parts);
+  if (n <= 32) return launch<T, V, 32, 1, SHIFT>(a, bwd, st, parts);
+  if (n <= 64) return launch<T, V, 32, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 128) return launch<T, V, 64, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 256) return launch<T, V, 128, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 512) return launch<T, V, 256, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 1024) return launch<T, V, 512, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 2048) return launch<T, V, 1024, 2, SHIFT>(a, bwd, st, parts);
+  return launch<T, V, 1024, V == 8 ? 3 : SHIFT ? 5 : 4, SHIFT>(a, bwd, st, parts);
+}
 template <typename T> int dispatch(const Args& a, bool vec, bool bwd, cudaStream_t st, int* parts) {
   constexpr int V = 16 / sizeof(T);
-  const int n = vec ? a.D / V : a.D;
-  if (vec) {
-    if (n <= 8) return launch<T, V, 8, 1>(a, bwd, st, parts);
-    if (n <= 16) return launch<T, V, 16, 1>(a, bwd, st, parts);
-    if (n <= 32) return launch<T, V, 32, 1>(a, bwd, st, parts);
-    if (n <= 64) return launch<T, V, 32, 2>(a, bwd, st, parts);
-    if (n <= 128) return launch<T, V, 64, 2>(a, bwd, st, parts);
-    if (n <= 256) return launch<T, V, 128, 2>(a, bwd, st, parts);
-    if (n <= 512) return launch<T, V, 256, 2>(a, bwd, st, parts);
-    if (n <= 1024) return launch<T, V, 512, 2>(a, bwd, st, parts);
-    if (n <= 2048) return launch<T, V, 1024, 2>(a, bwd, st, parts);
-    return launch<T, V, 1024, 4>(a, bwd, st, parts);
-  }
-  if (n <= 128) return launch<T, 1, 32, 4>(a, bwd, st, parts);
-  if (n <= 512) return launch<T, 1, 128, 4>(a, bwd, st, parts);
-  if (n <= 2048) return launch<T, 1, 256, 8>(a, bwd, st, parts);
-  if (n <= 8192) return launch<T, 1, 1024, 8>(a, bwd, st, parts);
-  return launch<T, 1, 1024, 16>(a, bwd, st, parts);
+  if (vec && a.shift == 0 && a.D % V == 0) return dispatch_rows<T, V, false>(a, bwd, st, parts);
+  if (vec) return dispatch_rows<T, V, true>(a, bwd, st, parts);
+  if (a.D <= 128) return launch<T, 1, 32, 4, false>(a, bwd, st, parts);
+  if (a.D <= 1024) return launch<T, 1, 128, 8, false>(a, bwd, st, parts);
+  return launch<T, 1, 1024, 16, false>(a, bwd, st, parts);
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+int past16(const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) % 16); }
 
 int check(long long rows, int D, float eps, int mode) {
   if (rows <= 0 || D <= 0 || !(eps >= 0.f) || isinf(eps)) return INFINI_ERR_INVALID_ARG;
@@ -456,8 +518,9 @@ int infini_attn_layer_norm_forward(const void* x, const void* weight, const void
   a.D = D;
   a.eps = eps;
   a.w32 = (mode & INFINI_WEIGHT_F32) != 0;
-  const bool vec = D % (16 / es) == 0 && ln::aligned16(x) && ln::aligned16(y) && ln::aligned16(weight) &&
-                   (!bias || ln::aligned16(bias));
+  a.shift = ln::past16(x) / (int)es;
+  // whole vectors of the weights only where rows are whole vectors too
+  const bool vec = ln::past16(x) == ln::past16(y) && (a.shift != 0 || D % (16 / es) != 0 || (ln::past16(weight) == 0 && ln::past16(bias) == 0));
   return (mode & INFINI_F32) ? ln::dispatch<float>(a, vec, false, stream, nullptr)
                              : ln::dispatch<__nv_bfloat16>(a, vec, false, stream, nullptr);
 }
@@ -504,7 +567,9 @@ int infini_attn_layer_norm_backward(const void* x, const void* weight, const voi
   a.D = D;
   a.eps = eps;
   a.w32 = (mode & INFINI_WEIGHT_F32) != 0;
-  const bool vec = D % (16 / es) == 0 && ln::aligned16(x) && ln::aligned16(dy) && ln::aligned16(dx) && ln::aligned16(weight);
+  a.shift = ln::past16(x) / (int)es;
+  const bool vec = ln::past16(x) == ln::past16(dy) && ln::past16(x) == ln::past16(dx) &&
+                   (a.shift != 0 || D % (16 / es) != 0 || ln::past16(weight) == 0);
   int parts = 0;
   rc = (mode & INFINI_F32) ? ln::dispatch<float>(a, vec, true, stream, &parts)
                            : ln::dispatch<__nv_bfloat16>(a, vec, true, stream, &parts);

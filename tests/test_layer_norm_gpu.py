@@ -77,6 +77,26 @@ def test_sizes(rows, D, t, wt):
 
 
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(9001, 77), (5003, 1001), (2500, 2341), (1201, 8190), (20000, 12), (7, 16379)])
+def test_many_rows_that_start_anywhere(rows, D, t):
+    x, w, b, dy = make(rows, D, t, t, rows)
+    y = torch.full_like(x, float("nan"))
+    api.infini_attn_layer_norm_forward(x, w, b, y)
+    check_forward(x, w, b, y, 1e-5)
+    check_backward(x, w, dy, api.infini_attn_layer_norm_backward(x, w, dy), 1e-5)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+def test_tensors_on_different_grids(t):
+    x, w, b, _ = make(50, 130, t, t, 5)
+    for shift in (1, 3):
+        y = torch.zeros(50 * 130 + 8, dtype=t, device=DEV)
+        api.infini_attn_layer_norm_forward(x, w, b, y[shift:shift + 50 * 130].view(50, 130))
+        check_forward(x, w, b, y[shift:shift + 50 * 130].view(50, 130), 1e-5)
+        assert not y[:shift].any() and not y[shift + 50 * 130:].any()
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
 def test_pointers_off_alignment(t):
     x, w, b, dy = make(11, 512, t, t, 3, shift=1)
     y = torch.empty(11 * 512 + 1, dtype=t, device=DEV)[1:].view(11, 512)
