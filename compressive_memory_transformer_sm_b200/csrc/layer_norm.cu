@@ -164,7 +164,7 @@ struct Args {
 template <int TPR> constexpr int kBlockThreads = TPR < 128 ? 128 : TPR;
 // Elements per thread up to which the weights stay in registers for all the rows of a block.
 // (Re-read for each row they cost four times the row itself from L2: 146 us at 32768 x 4096 bf16.)
-constexpr int kKeep = 16;
+constexpr int kKeep = 24;
 
 // Column of element 0 of a thread's vector v.  SHIFT: rows do not start on 16 bytes; a row's vectors
 // then are those of memory, the first starting `off` elements before the row, so that all but the
@@ -466,10 +466,15 @@ template <typename T, int V, bool SHIFT> int dispatch_rows(const Args& a, bool b
   if (n <= 16) return launch<T, V, 16, 1, SHIFT>(a, bwd, st, parts);
   if (n <= 32) return launch<T, V, 32, 1, SHIFT>(a, bwd, st, parts);
   if (n <= 64) return launch<T, V, 32, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 96) return launch<T, V, 32, 3, SHIFT>(a, bwd, st, parts);
   if (n <= 128) return launch<T, V, 64, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 192) return launch<T, V, 64, 3, SHIFT>(a, bwd, st, parts);
   if (n <= 256) return launch<T, V, 128, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 384) return launch<T, V, 128, 3, SHIFT>(a, bwd, st, parts);
   if (n <= 512) return launch<T, V, 256, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 768) return launch<T, V, 256, 3, SHIFT>(a, bwd, st, parts);
   if (n <= 1024) return launch<T, V, 512, 2, SHIFT>(a, bwd, st, parts);
+  if (n <= 1536) return launch<T, V, 512, 3, SHIFT>(a, bwd, st, parts);
   if (n <= 2048) return launch<T, V, 1024, 2, SHIFT>(a, bwd, st, parts);
   return launch<T, V, 1024, V == 8 ? 3 : SHIFT ? 5 : 4, SHIFT>(a, bwd, st, parts);
 }
