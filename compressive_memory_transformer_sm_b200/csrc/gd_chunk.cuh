@@ -501,6 +501,7 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
       if (MODE == kPassSnap) state_snap<ND>(S, a.snap + (((bh * a.nc + first + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // R^T = S^T K^T, Y^T = S^T Q^T
       float R[NB][2][4] = {}, Y[NB][2][4] = {}, lo[NB][2][4] = {};
+      float yl[NB][2][4] = {};  // low order sums of Y, where it is not rounded to bf16 in the end
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
         AFrag<3> fs;
@@ -517,7 +518,11 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
             for (int p = 0; p < PO; ++p)
 #pragma unroll
               for (int y = 0; y < 4; ++y) fo.r[p][y] = fs.r[p][y];
-            mma2(Y[x][0], Y[x][1], fo, load_b_k2(s.q, LD, tile(x, 0), tile(x, 1), 16 * kk, lane));
+            const auto fq = load_b_k2(s.q, LD, tile(x, 0), tile(x, 1), 16 * kk, lane);
+            if constexpr (PI > 1)
+              mma2(Y[x][0], Y[x][1], yl[x][0], yl[x][1], fo, fq);
+            else
+              mma2(Y[x][0], Y[x][1], fo, fq);
           }
         }
       }
@@ -598,7 +603,10 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
           for (int y = 0; y < 2; ++y) {
             const float2 gam = vec2(0, tile(x, y));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Y[x][y][e] *= e & 1 ? gam.y : gam.x;
+            for (int e = 0; e < 4; ++e) {
+              Y[x][y][e] = (e & 1 ? gam.y : gam.x) * (PI > 1 ? Y[x][y][e] + yl[x][y][e] : Y[x][y][e]);
+              yl[x][y][e] = 0.f;
+            }
           }
         if constexpr (KS > 1) {
           BFrag<PO> fp[4];
@@ -607,23 +615,23 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
             fu[kk] = get_frag<PO>(ex.U[kk][0], lane);
             fp[kk] = load_tri_k2<PO>(s.P, tile(0, 0), tile(0, 1), kk, lane);
           }
-          float yl[2][4] = {};
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk <= tile(0, 0) >> 1)
-              mma2(Y[0][0], Y[0][1], yl[0], yl[1], fu[kk], fp[kk]);
+              mma2(Y[0][0], Y[0][1], yl[0][0], yl[0][1], fu[kk], fp[kk]);
             else if (kk <= tile(0, 1) >> 1)
-              mma1(Y[0][1], yl[1], fu[kk], fp[kk], 1);
+              mma1(Y[0][1], yl[0][1], fu[kk], fp[kk], 1);
           }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) Y[0][y][e] += yl[y][e];
         } else {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-            for (int x = kk; x < NB; ++x) mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, x, kk, lane));
+            for (int x = kk; x < NB; ++x) {
+              if constexpr (PI > 1)
+                mma2(Y[x][0], Y[x][1], yl[x][0], yl[x][1], fu[kk], load_tri_k<PO>(s.P, x, kk, lane));
+              else
+                mma2(Y[x][0], Y[x][1], fu[kk], load_tri_k<PO>(s.P, x, kk, lane));
+            }
         }
         __syncwarp();  // every lane has taken its v
         const int n = chunk_len(len, (long long)a.c0 + first + i), w = min(16, a.dv - v0);
@@ -633,7 +641,7 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Y[x][y][e] *= a.scale;
+            for (int e = 0; e < 4; ++e) Y[x][y][e] = a.scale * (KS > 1 || PI > 1 ? Y[x][y][e] + yl[x][y][e] : Y[x][y][e]);
             store_tile_t(sv + 8 * tile(x, y) * ldv + vs, ldv, Y[x][y], lane);
           }
         __syncwarp();
@@ -1015,20 +1023,35 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
       float R[8][4] = {}, Y[8][4] = {}, W[8][4] = {}, dot = 0.f;
       const float4* ps = snap + warp * (DK / 8) * 32 + lane;
       const float4* pd = dsnap + warp * (DK / 8) * 32 + lane;
-#pragma unroll 2
-      for (int kk = 0; kk < DK / 16; ++kk) {
-        const float4 s0 = ps[2 * kk * 32], s1 = ps[(2 * kk + 1) * 32], d0 = pd[2 * kk * 32], d1 = pd[(2 * kk + 1) * 32];
-        dot += s0.x * d0.x + s0.y * d0.y + s0.z * d0.z + s0.w * d0.w + s1.x * d1.x + s1.y * d1.y + s1.z * d1.z + s1.w * d1.w;
-        const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
-        const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
-        const AFrag<3> fs = from_acc<3>(sa, sb), fd = from_acc<3>(da, db);
+      // two token halves, so that the low order sums find room
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          const BFrag<PI> bk = load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane);
-          mma2(R[2 * np], R[2 * np + 1], fs, bk);
-          mma2(W[2 * np], W[2 * np + 1], fd, bk);
-          mma2(Y[2 * np], Y[2 * np + 1], fs, load_b_k<PI>(s.q, LD, 16 * np, 16 * kk, lane));
+      for (int half = 0; half < 2; ++half) {
+        float rl[4][4] = {}, yl[4][4] = {}, wl[4][4] = {};
+#pragma unroll 2
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          const float4 s0 = ps[2 * kk * 32], s1 = ps[(2 * kk + 1) * 32], d0 = pd[2 * kk * 32], d1 = pd[(2 * kk + 1) * 32];
+          if (half == 0)
+            dot += s0.x * d0.x + s0.y * d0.y + s0.z * d0.z + s0.w * d0.w + s1.x * d1.x + s1.y * d1.y + s1.z * d1.z + s1.w * d1.w;
+          const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
+          const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
+          const AFrag<3> fs = from_acc<3>(sa, sb), fd = from_acc<3>(da, db);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int np = 2 * half + x;
+            const BFrag<PI> bk = load_b_k<PI>(s.k, LD, 16 * np, 16 * kk, lane);
+            mma2(R[2 * np], R[2 * np + 1], rl[2 * x], rl[2 * x + 1], fs, bk);
+            mma2(W[2 * np], W[2 * np + 1], wl[2 * x], wl[2 * x + 1], fd, bk);
+            mma2(Y[2 * np], Y[2 * np + 1], yl[2 * x], yl[2 * x + 1], fs, load_b_k<PI>(s.q, LD, 16 * np, 16 * kk, lane));
+          }
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            R[4 * half + x][e] += rl[x][e];
+            Y[4 * half + x][e] += yl[x][e];
+            W[4 * half + x][e] += wl[x][e];
+          }
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -1050,7 +1073,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
             Y[x][2 * r + e] = vv - s.vec[t] * R[x][2 * r + e];
           }
         }
-      float U[8][4] = {};
+      float U[8][4] = {}, lo[8][4] = {};
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         float xa[4], xb[4];
@@ -1062,7 +1085,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
         const AFrag<3> fx = from_acc<3>(xa, xb);
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          if (np >= kk) mma2(U[2 * np], U[2 * np + 1], fx, load_b_k<3>(s.Tm, kLdT, 16 * np, 16 * kk, lane));
+          if (np >= kk) mma2(U[2 * np], U[2 * np + 1], lo[2 * np], lo[2 * np + 1], fx, load_b_k<3>(s.Tm, kLdT, 16 * np, 16 * kk, lane));
       }
       float sum_e[16];
 #pragma unroll
@@ -1070,6 +1093,9 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = 8 * x + c2 + e;
+          U[x][e] += lo[x][e];
+          U[x][2 + e] += lo[x][2 + e];
+          lo[x][e] = lo[x][2 + e] = 0.f;
           sum_e[2 * x + e] = s.vec[64 + t] * (W[x][e] * U[x][e] + W[x][2 + e] * U[x][2 + e]);
           s.U[t * kLdU + 16 * warp + g] = U[x][e];
           s.U[t * kLdU + 16 * warp + g + 8] = U[x][2 + e];
@@ -1081,21 +1107,21 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
         const AFrag<PI> fd = load_a_m<PI>(s.d, LDD, 16 * kk, 16 * warp, lane);
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          if (np <= kk) mma2(U[2 * np], U[2 * np + 1], fd, load_b_n<3>(s.P, kLdT, 16 * kk, 16 * np, lane));
+          if (np <= kk) mma2(U[2 * np], U[2 * np + 1], lo[2 * np], lo[2 * np + 1], fd, load_b_n<3>(s.P, kLdT, 16 * kk, 16 * np, lane));
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          U[x][e] = a.scale * U[x][e] + s.vec[64 + 8 * x + c2 + (e & 1)] * W[x][e];
-          W[x][e] = 0.f;
+          U[x][e] = a.scale * (U[x][e] + lo[x][e]) + s.vec[64 + 8 * x + c2 + (e & 1)] * W[x][e];
+          W[x][e] = lo[x][e] = 0.f;
         }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const AFrag<3> fu = from_acc<3>(U[2 * kk], U[2 * kk + 1]);
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          if (np <= kk) mma2(W[2 * np], W[2 * np + 1], fu, load_b_n<3>(s.Tm, kLdT, 16 * kk, 16 * np, lane));
+          if (np <= kk) mma2(W[2 * np], W[2 * np + 1], lo[2 * np], lo[2 * np + 1], fu, load_b_n<3>(s.Tm, kLdT, 16 * kk, 16 * np, lane));
       }
       float sum_b[16];
 #pragma unroll
@@ -1103,6 +1129,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = 8 * x + c2 + e;
+          W[x][e] += lo[x][e];
+          W[x][2 + e] += lo[x][2 + e];
           sum_a[2 * x + e] -= s.vec[128 + t] * s.vec[t] * (W[x][e] * R[x][e] + W[x][2 + e] * R[x][2 + e]);
           sum_b[2 * x + e] = W[x][e] * Y[x][e] + W[x][2 + e] * Y[x][2 + e];
           s.X[t * kLdU + 16 * warp + g] = W[x][e];
@@ -1121,7 +1149,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
       }
       const int rb = warp & 3, m0 = 16 * rb;
       const bool is_a = warp >= 4;
-      float acc[4][2][4] = {}, kk2[4][2][4] = {};
+      float acc[4][2][4] = {}, kk2[4][2][4] = {}, lo[4][2][4] = {};
       for (int kk = 0; kk < nw; ++kk) {
         AFrag<3> fx;
         AFrag<PI> fd;
@@ -1134,9 +1162,9 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
           if (cb <= rb) {
             const BFrag<3> fu = load_b_k<3>(s.U, kLdU, 16 * cb, 16 * kk, lane);
             if (is_a)
-              mma2(acc[cb][0], acc[cb][1], fx, fu);
+              mma2(acc[cb][0], acc[cb][1], lo[cb][0], lo[cb][1], fx, fu);
             else
-              mma2(acc[cb][0], acc[cb][1], fd, fu);
+              mma2(acc[cb][0], acc[cb][1], lo[cb][0], lo[cb][1], fd, fu);
           }
       }
       if (is_a)
@@ -1157,7 +1185,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
-              const float x = acc[cb][t][e];
+              const float x = acc[cb][t][e] + lo[cb][t][e];
               if (is_a) {
                 const float dec = decay(s.G[i], s.G[jj], i > jj), be = s.vec[128 + i];
                 const float ab = -x * dec * kk2[cb][t][e];
@@ -1233,17 +1261,17 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
     }
     if (warp < DK / 16) {
       const int n0 = 16 * warp;
-      float Q[4][2][4] = {}, K[4][2][4] = {};
+      float Q[4][2][4] = {}, K[4][2][4] = {}, ql[4][2][4] = {}, kl[4][2][4] = {};
       for (int kw = 0; kw < nw; ++kw) {
         const BFrag<PO> fs = load_b_state<PO>(reinterpret_cast<const float*>(snap + kw * (DK / 8) * 32), n0, lane);
         const BFrag<PO> fd = load_b_state<PO>(reinterpret_cast<const float*>(dsnap + kw * (DK / 8) * 32), n0, lane);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
           const int t = 16 * mt + g;
-          mma2(Q[mt][0], Q[mt][1], load_a_k<PI>(s.d, LDD, 16 * mt, 16 * kw, lane), fs);
-          mma2(K[mt][0], K[mt][1],
+          mma2(Q[mt][0], Q[mt][1], ql[mt][0], ql[mt][1], load_a_k<PI>(s.d, LDD, 16 * mt, 16 * kw, lane), fs);
+          mma2(K[mt][0], K[mt][1], kl[mt][0], kl[mt][1],
                load_a_k<PO>(s.X, kLdU, 16 * mt, 16 * kw, lane, -s.vec[128 + t] * s.vec[t], -s.vec[136 + t] * s.vec[t + 8]), fs);
-          mma2(K[mt][0], K[mt][1], load_a_k<PO>(s.U, kLdU, 16 * mt, 16 * kw, lane, s.vec[64 + t], s.vec[72 + t]), fd);
+          mma2(K[mt][0], K[mt][1], kl[mt][0], kl[mt][1], load_a_k<PO>(s.U, kLdU, 16 * mt, 16 * kw, lane, s.vec[64 + t], s.vec[72 + t]), fd);
         }
       }
 #pragma unroll
@@ -1251,15 +1279,18 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) Q[mt][t][e] *= a.scale * s.vec[16 * mt + g + 8 * (e >> 1)];
+          for (int e = 0; e < 4; ++e) {
+            Q[mt][t][e] = (Q[mt][t][e] + ql[mt][t][e]) * (a.scale * s.vec[16 * mt + g + 8 * (e >> 1)]);
+            ql[mt][t][e] = 0.f;
+          }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const BFrag<PI> bk = load_b_n<PI>(s.k, LD, 16 * kk, n0, lane), bq = load_b_n<PI>(s.q, LD, 16 * kk, n0, lane);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          if (kk <= mt) mma2(Q[mt][0], Q[mt][1], load_a_k<PO>(s.P, kLdT, 16 * mt, 16 * kk, lane), bk);
-          mma2(K[mt][0], K[mt][1], load_a_k<PO>(s.Tm, kLdT, 16 * mt, 16 * kk, lane), bk);
-          if (kk >= mt) mma2(K[mt][0], K[mt][1], load_a_m<PO>(s.P, kLdT, 16 * kk, 16 * mt, lane), bq);
+          if (kk <= mt) mma2(Q[mt][0], Q[mt][1], ql[mt][0], ql[mt][1], load_a_k<PO>(s.P, kLdT, 16 * mt, 16 * kk, lane), bk);
+          mma2(K[mt][0], K[mt][1], kl[mt][0], kl[mt][1], load_a_k<PO>(s.Tm, kLdT, 16 * mt, 16 * kk, lane), bk);
+          if (kk >= mt) mma2(K[mt][0], K[mt][1], kl[mt][0], kl[mt][1], load_a_m<PO>(s.P, kLdT, 16 * kk, 16 * mt, lane), bq);
         }
       }
       float* acc = a.acc + (((long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
@@ -1270,7 +1301,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int tk = 16 * mt + g + 8 * r, x = n0 + 8 * t + c2;
-            float2 yq = make_float2(Q[mt][t][2 * r], Q[mt][t][2 * r + 1]), yk = make_float2(K[mt][t][2 * r], K[mt][t][2 * r + 1]);
+            float2 yq = make_float2(Q[mt][t][2 * r] + ql[mt][t][2 * r], Q[mt][t][2 * r + 1] + ql[mt][t][2 * r + 1]);
+            float2 yk = make_float2(K[mt][t][2 * r] + kl[mt][t][2 * r], K[mt][t][2 * r + 1] + kl[mt][t][2 * r + 1]);
             if (a.group > 1) {  // the same thread holds this element for every value head of the key head
               float2* pq = reinterpret_cast<float2*>(acc + tk * DK + x);
               float2* pk = reinterpret_cast<float2*>(acc + (kC + tk) * DK + x);
