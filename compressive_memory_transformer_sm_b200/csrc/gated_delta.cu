@@ -271,8 +271,13 @@ template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
     return GD_LAUNCH((grad_kernel<T, DK>), chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
 }
 
-// Sequences of fewer tokens than this go token by token.
-constexpr long long kChunkFrom = 32;
+// Sequences of fewer tokens than this go token by token (128 x 128, microseconds, tokens against a chunk of 64: bf16, 8
+// heads, 20 tokens 13.4 / 13.8; 128 heads, 10 tokens 20.5 / 22.6, 16 tokens 30.7 / 22.6; fp32, 8 heads, 31 tokens
+// 19.3 / 22.2; 128 heads 57 / 72).
+long long chunk_from(const Shape& s) {
+  if (s.mode & INFINI_F32) return 36;
+  return (long long)s.B * s.H <= kSms / 4 ? 20 : 11;
+}
 
 int forward(infini_attn_gated_delta_params p) {
   if (!p.q || !p.k || !p.v || !p.g || !p.beta || !p.S || !p.out) return INFINI_ERR_INVALID_ARG;
@@ -307,7 +312,7 @@ int forward(infini_attn_gated_delta_params p) {
   if (rc != INFINI_OK) return rc;
   const Shape shape{p.B, p.H, p.Hk, p.dk, p.dv, p.mode, p.L};
   const float scale = p.scale != 0.f ? p.scale : 1.f / sqrtf((float)p.dk);
-  if (p.L >= kChunkFrom) {
+  if (p.L >= chunk_from(shape)) {
     const long long slab = slab_chunks(shape);
     const ChunkSpace space(shape, slab, false);
     void* w = p.workspace;
@@ -471,7 +476,7 @@ int infini_attn_gated_delta_forward(const infini_attn_gated_delta_params* p) {
 size_t infini_attn_gated_delta_workspace_size(const infini_attn_gated_delta_params* p) {
   if (!p) return 0;
   const gd::Shape s{p->B, p->H, p->Hk, p->dk, p->dv, p->mode, p->L};
-  if (gd::check_shape(s) != INFINI_OK || p->L < gd::kChunkFrom) return 0;
+  if (gd::check_shape(s) != INFINI_OK || p->L < gd::chunk_from(s)) return 0;
   return gd::ChunkSpace(s, gd::slab_chunks(s), false).bytes;
 }
 

@@ -61,7 +61,7 @@ def check_forward(q, k, v, g, beta, S0, out, S, scale=0.0, lens=None):
 
 SHAPES = [  # B, H, Hk, L, dk, dv
     (1, 1, 1, 1, 128, 128), (2, 2, 1, 3, 16, 16), (1, 3, 3, 63, 128, 128), (1, 2, 2, 64, 64, 64), (1, 2, 1, 65, 128, 64),
-    (2, 4, 2, 130, 33, 50), (1, 2, 2, 200, 96, 100), (1, 1, 1, 257, 128, 128), (1, 4, 1, 129, 1, 1), (1, 2, 2, 100, 7, 128),
+    (2, 4, 2, 130, 33, 50), (2, 8, 8, 19, 128, 128), (1, 2, 2, 20, 128, 64), (1, 2, 1, 36, 64, 128), (1, 2, 2, 200, 96, 100), (1, 1, 1, 257, 128, 128), (1, 4, 1, 129, 1, 1), (1, 2, 2, 100, 7, 128),
     (1, 2, 1, 77, 128, 3), (1, 1, 1, 1100, 128, 128),
 ]
 
