@@ -1482,23 +1482,15 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+          store_parts_t(s.U + (16 * blks[x] + 8 * t) * kLdG + 16 * strip, kPlaneG, kLdG, U[x][t], lane);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int tk = 16 * blks[x] + 8 * t + c2 + e;
             sum[x][t][e] = s.vec[64 + tk] * (W[x][t][e] * U[x][t][e] + W[x][t][2 + e] * U[x][t][2 + e]);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float y = U[x][t][2 * r + e];
-#pragma unroll
-              for (int p = 0; p < 3; ++p) {
-                const bf16 w = from_f32<bf16>(y);
-                s.U[p * kPlaneG + tk * kLdG + v0 + 8 * r] = w;
-                y -= to_f32(w);
-              }
-              U[x][t][2 * r + e] = 0.f;
-            }
+            U[x][t][e] = U[x][t][2 + e] = 0.f;
           }
+        }
       sum_tokens(sum, s.tok[strip][1], blks[0], blks[1], lane);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
@@ -1547,18 +1539,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tk = 16 * blks[x] + 8 * t + c2 + (e & 1);
-            float y = W[x][t][e];
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              const bf16 w = from_f32<bf16>(y);
-              s.X[p * kPlaneG + tk * kLdG + 16 * strip + g + 8 * (e >> 1)] = w;
-              y -= to_f32(w);
-            }
-          }
+        for (int t = 0; t < 2; ++t) store_parts_t(s.X + (16 * blks[x] + 8 * t) * kLdG + 16 * strip, kPlaneG, kLdG, W[x][t], lane);
     __syncthreads();
     // ---- 2: a 16 x 16 block of dA in each of warps 0-9, one or two of dP in the others; dV
     {
@@ -1685,16 +1666,21 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i, tb = t >> 4, tl = t & 15;
         float av = 0.f, ev = 0.f, bv = 0.f, pos = 0.f, neg = 0.f;
-        for (int w = 0; w < nw; ++w) {
-          av += s.tok[w][0][t];
-          ev += s.tok[w][1][t];
-          bv += s.tok[w][2][t];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {  // every load in flight; what lies behind nw is not added
+          const float x0 = s.tok[w][0][t], x1 = s.tok[w][1][t], x2 = s.tok[w][2][t];
+          av += w < nw ? x0 : 0.f;
+          ev += w < nw ? x1 : 0.f;
+          bv += w < nw ? x2 : 0.f;
         }
-        for (int c = 0; c <= tb; ++c) {
-          pos += s.rowP[tri_block(tb, c)][tl] + s.rowA[tri_block(tb, c)][tl];
-          bv += s.rowB[tri_block(tb, c)][tl];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int above = tri_block(tb, min(c, tb)), below = tri_block(max(c, tb), tb);
+          const float x0 = s.rowP[above][tl] + s.rowA[above][tl], x1 = s.rowB[above][tl], x2 = s.colP[below][tl] + s.colA[below][tl];
+          pos += c <= tb ? x0 : 0.f;
+          bv += c <= tb ? x1 : 0.f;
+          neg += c >= tb ? x2 : 0.f;
         }
-        for (int r = tb; r < 4; ++r) neg += s.colP[tri_block(r, tb)][tl] + s.colA[tri_block(r, tb)][tl];
         x[i] = (double)av - ev + pos - neg;
         sum_e += ev;
         if (t < rows) a.dbeta[r0 + t] = t < n ? bv : 0.f;

@@ -320,6 +320,17 @@ __device__ __forceinline__ void store_tile_t(bf16* m, int ld, const float (&d)[4
                "r"(pack_bf16x2(d[0], d[1])), "r"(pack_bf16x2(d[2], d[3]))
                : "memory");
 }
+// ... in three parts, each a plane
+__device__ __forceinline__ void store_parts_t(bf16* m, int plane, int ld, const float (&d)[4], int lane) {
+  uint32_t r[3][4];
+  split<3>(d[0], d[1], r, 0);
+  split<3>(d[2], d[3], r, 1);
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(smem_u32(m + p * plane + (lane & 7) * ld + (lane & 8))),
+                 "r"(r[p][0]), "r"(r[p][1])
+                 : "memory");
+}
 template <int P> __device__ __forceinline__ AFrag<P> get_frag(const uint4* src, int lane) {
   AFrag<P> a;
 #pragma unroll
