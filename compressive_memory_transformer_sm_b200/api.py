@@ -474,12 +474,12 @@ def _tensors(where: str, table):
             if not t.is_contiguous():
                 raise ValueError(f"{where}: {name} must be contiguous")
         else:
-            stride = t.stride()
+            stride, rows = t.stride(), t.numel()
             if layout == "r":
                 if stride[-1] != 1 and shape[-1] > 1:
                     raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
-                stride = stride[:-1]
-            if not any(stride) and t.numel() > shape[-1]:
+                stride, rows = stride[:-1], rows // max(1, shape[-1])
+            if rows > 1 and not any(stride):
                 raise ValueError(f"{where}: {name} must not be broadcast along every dimension")
     dev = table[0][1].get_device()
     for name, t, _, _, _ in table:

@@ -228,7 +228,7 @@ template <typename T, int DK, int MODE> int run_forward(ChunkArgs a, int segment
 template <typename T, int DK, bool SEG> int run_both(ChunkArgs a, int strips, cudaStream_t st) {
   const StatePlan p = state_plan<T, DK, 3>(strips, 2LL * a.B * a.H * a.nseg);
   take_plan(a, p);
-  const dim3 grid(2 * p.blocks * a.nseg, a.H, a.B);
+  const dim3 grid(p.blocks * a.nseg, a.H, 2 * a.B);
   return p.KS == 4 ? GD_LAUNCH((both_kernel<T, DK, 4, SEG>), grid, p.threads, p.smem, kPhaseBwd, a, st)
                    : GD_LAUNCH((both_kernel<T, DK, 1, SEG>), grid, p.threads, p.smem, kPhaseBwd, a, st);
 }
@@ -365,6 +365,7 @@ int backward(infini_attn_gated_delta_backward_params p) {
   if (!fits(p.q_stride, p.B, p.Hk, p.L) || !fits(p.k_stride, p.B, p.Hk, p.L) || !fits(p.v_stride, p.B, p.H, p.L) ||
       !fits(p.d_out_stride, p.B, p.H, p.L) || !fits(p.g_stride, p.B, p.H, p.L) || !fits(p.beta_stride, p.B, p.H, p.L))
     return INFINI_ERR_INVALID_ARG;
+  if (p.B > 32767) return INFINI_ERR_UNSUPPORTED;  // two grid rows per batch row
   const bool f32 = (p.mode & INFINI_F32) != 0;
   const size_t es = f32 ? 4 : 2, tok = (size_t)p.B * p.L, nS = (size_t)p.B * p.H * p.dk * p.dv * 4;
   struct Range {

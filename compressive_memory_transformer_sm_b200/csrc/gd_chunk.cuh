@@ -873,14 +873,15 @@ constexpr int state_threads(int KS) { return KS == 4 ? 384 : 256; }
 template <typename T, int DK, int KS, int MODE> __global__ void __launch_bounds__(state_threads(KS)) forward_kernel(const ChunkArgs a) {
   state_pass<T, DK, KS, MODE, Dims<T, DK>::kOut>(a, blockIdx.x % a.blocks, blockIdx.x / a.blocks, blockIdx.y, blockIdx.z);
 }
-// The two passes of the backward do not depend on each other: even blocks run the states forward,
-// odd ones their gradients backward.
+// The two passes of the backward do not depend on each other: the first half of the grid (z) runs the
+// states forward, the second their gradients backward.  (Neighbouring blocks of the two on one SM
+// evict each other's instructions: "no instruction" was a fifth of the stalls at 128 (b, h).)
 template <typename T, int DK, int KS, bool SEG> __global__ void __launch_bounds__(state_threads(KS)) both_kernel(const ChunkArgs a) {
-  const int x = blockIdx.x >> 1;
-  if (blockIdx.x & 1)
-    bwd_state_pass<T, DK, KS, SEG>(a, x % a.blocks, x / a.blocks, blockIdx.y, blockIdx.z);
+  const int vblock = blockIdx.x % a.blocks, seg = blockIdx.x / a.blocks;
+  if ((int)blockIdx.z >= a.B)
+    bwd_state_pass<T, DK, KS, SEG>(a, vblock, seg, blockIdx.y, blockIdx.z - a.B);
   else
-    state_pass<T, DK, KS, SEG ? kPassSeg : kPassSnap, 3>(a, x % a.blocks, x / a.blocks, blockIdx.y, blockIdx.z);
+    state_pass<T, DK, KS, SEG ? kPassSeg : kPassSnap, 3>(a, vblock, seg, blockIdx.y, blockIdx.z);
 }
 
 // The states between segments from what each makes of a zero state (in segS, segD) and of the unit

@@ -168,6 +168,9 @@ def test_binding_refuses_what_it_cannot_pass_on():
         api.infini_attn_gated_delta_forward(q, k, v, g, g[:, :1], S, z(1, 2, 4, 8))
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         api.infini_attn_gated_delta_forward(q.half(), k, v, g, g, S, v)
+    one = torch.tensor(0.0).expand(1, 1, 4)  # one element for four tokens
+    with pytest.raises(ValueError, match="broadcast"):
+        api.infini_attn_gated_delta_forward(q[:, :1], k[:, :1], v[:, :1], one, g[:, :1], S[:, :1].contiguous(), v[:, :1])
     with pytest.raises(ValueError, match="broadcast"):
         api.infini_attn_gated_delta_forward(q, k, v, torch.tensor(0.0).expand(1, 2, 4), g, S, z(1, 2, 4, 8))
     with pytest.raises(TypeError):
