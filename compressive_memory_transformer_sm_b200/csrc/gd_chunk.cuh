@@ -422,6 +422,17 @@ template <int KS> __device__ __forceinline__ void group_sync(int group) {
     __syncwarp();
 }
 
+// The passes, forward (state_pass) and backward (bwd_state_pass).  What bounds them is the chain
+// K S -> X -> U -> S of each chunk on the tensor cores: per chunk and 16 value columns of a 128-row
+// state 692 products of 16 x 8 x 16 with outputs (192 K S, 128 Q S, 120 T X, 60 P U, 192 K^T U; blocks
+// above the diagonal are skipped), 8 cycles each on one of four sub-cores.  KS 1: 128 (b, h) x
+// 64 chunks in 520 us, the tensor pipe 52 % of the time active; two blocks to an SM, so that one's
+// loads and conversions run beside the other's products (one block of eight warps: 650 us, its warps
+// all do the same at the same time).  KS 4: 8 (b, h) x 512 chunks in 1170 us, 2.3 us a chunk, of
+// which products are 0.7 us; one warp per sub-core leaves every latency open.  Warps that only copy
+// took the copies (3500 of 7300 cycles) off that chain; a bulk copy per row by one warp cost more
+// (2.2 times the whole pass), for the row count of such copies.
+
 // What a pass over the chunks of a segment leaves behind.
 enum Pass {
   kPassOut,   // outputs, and S after the row's last chunk
@@ -1336,6 +1347,9 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 }
 
 // ------------------------------------------------------------------ gradients, bf16
+// Bound by the tensor pipe and what feeds it: 26 thousand cycles of products in 54 thousand per chunk
+// and (b, h) (pipe active 48 %), at one block of 16 warps an SM for its 217 KB of operands.  4096
+// chunks in 893 us; with 8 warps that split the operands at each use 1770 us.
 // The same with 16 warps and every fp32 operand split once, where it is made: U and dX as three
 // planes [64][kLdG], T and P as they come, M + M^T and N as two.  Two warps share 16 value columns
 // (then 16 key columns): token blocks 0 and 3, or 1 and 2, so that the triangular products balance.

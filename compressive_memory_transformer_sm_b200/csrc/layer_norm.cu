@@ -11,6 +11,10 @@
 // loses it where |mean| is far above the spread), and the backward takes the statistics from the
 // row again instead of reading them.  All arithmetic and sums in fp32; y, dx and the weight
 // gradients are rounded once, to their tensors' types.
+//
+// Measured (bf16, of a 6544 GB/s copy): forward 32768 x 4096 98 us (84 %), 32768 x 1024 30 us (69 %);
+// backward 32768 x 4096 177 us (69 %), 32768 x 1024 55 us with its reduction (56 %; the issue slots
+// are two thirds busy with fp32 arithmetic and shuffles).  Odd rows: 32768 x 1025 57 and 111 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -185,7 +189,7 @@ __device__ __forceinline__ void load_row(Raw<T, VEC> (&r)[NV], const void* x, lo
     r[v] = Raw<T, VEC>{};
     if (!active || at >= a.D) continue;
     if constexpr (SHIFT)
-      if ((row == 0 && at < 0) || (row == a.rows - 1 && at + VEC > a.D)) {
+      if (row * a.D + at < 0 || row * a.D + at + VEC > a.rows * a.D) {
         r[v] = load_edge<VEC>(p + at, -at, a.D - at);
         continue;
       }

@@ -351,8 +351,17 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  * one after token lens[b] - 1, and their gradients are written as 0.
  *
  * All products and sums are fp32 or better, and so is the state; out, dq, dk
- * and dv are rounded once, to their type.  Results do not depend on the other
- * batch rows and heads, and repeat bit for bit.
+ * and dv are rounded once, to their type.  Results repeat bit for bit.  Short
+ * sequences are worked through token by token, longer ones in chunks of 64
+ * tokens, few long ones in segments side by side: the order of sums, and with
+ * it the last bits, goes by B, H, L and the types, never by the data.  Inside a
+ * chunk a NaN or infinity in k, v, g or beta also reaches the outputs of the
+ * chunk's earlier tokens.
+ *
+ * The forward's workspace stays below about 1 GiB however long the sequences
+ * are (it takes them in slabs).  The backward keeps the state and its gradient
+ * at every chunk: per token and value head 2 KB at 128 x 128, a little more
+ * with the rest.
  */
 typedef struct infini_attn_gated_delta_params {
   const void* q;
@@ -386,7 +395,7 @@ INFINI_API size_t infini_attn_gated_delta_workspace_size(const infini_attn_gated
  * after the last token, to dq, dk [B, Hk, L, dk] (summed over the value heads of a key head), dv [B, H, L, dv] (the
  * inputs' type), dg, dbeta [B, H, L] fp32 and (optional) dS0 [B, H, dk, dv] fp32; every output contiguous and
  * overlapping nothing else.  S0 is the state the forward started from (NULL: zero), dS_L NULL: zero.  d_out has
- * strides of its own.
+ * strides of its own.  B <= 32767.
  */
 typedef struct infini_attn_gated_delta_backward_params {
   const void* q;

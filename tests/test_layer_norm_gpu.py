@@ -77,7 +77,7 @@ def test_sizes(rows, D, t, wt):
 
 
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("rows,D", [(9001, 77), (5003, 1001), (2500, 2341), (1201, 8190), (20000, 12), (7, 16379)])
+@pytest.mark.parametrize("rows,D", [(9001, 77), (5003, 1001), (2500, 2341), (1201, 8190), (20000, 12), (7, 16379), (5, 1), (4001, 3), (9, 5)])
 def test_many_rows_that_start_anywhere(rows, D, t):
     x, w, b, dy = make(rows, D, t, t, rows)
     y = torch.full_like(x, float("nan"))
@@ -97,9 +97,10 @@ def test_tensors_on_different_grids(t):
 
 
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
-def test_pointers_off_alignment(t):
-    x, w, b, dy = make(11, 512, t, t, 3, shift=1)
-    y = torch.empty(11 * 512 + 1, dtype=t, device=DEV)[1:].view(11, 512)
+@pytest.mark.parametrize("rows,D", [(11, 512), (13, 1), (6, 3), (40, 77)])
+def test_pointers_off_alignment(rows, D, t):
+    x, w, b, dy = make(rows, D, t, t, 3, shift=1)
+    y = torch.empty(rows * D + 1, dtype=t, device=DEV)[1:].view(rows, D)
     api.infini_attn_layer_norm_forward(x, w, b, y)
     check_forward(x, w, b, y, 1e-5)
     check_backward(x, w, dy, api.infini_attn_layer_norm_backward(x, w, dy), 1e-5)
@@ -160,3 +161,28 @@ def test_stream_workspace_and_graph():
     torch.cuda.synchronize()
     check_forward(x, w, b, y, 1e-5)
     check_backward(x, w, dy, held, 1e-5)
+
+
+def test_norm_in_front_of_the_layer():
+    """The layer's pre-norm: a residual stream, normalised, through the projections and the memory, against the fp64
+    oracle of the layer on the oracle's norm rounded to bf16.  The layer's own tolerances (max-abs 2e-2, relative L2
+    5e-3) hold: an input that rounds the other way is one bf16 step off in one of D products."""
+    from compressive_memory_transformer_sm_b200 import DELTA
+    from compressive_memory_transformer_sm_b200 import workloads as W
+    from oracle import infini_ref as R
+
+    B, H, L, N, D = 1, 2, 384, 128, 256
+    x, w_qkv, w_o, beta = (t.to(DEV) for t in W.make_layer_inputs(B, H, L, D, seed=9300))
+    x = (3 * x + 1).contiguous()
+    w, b = (1 + 0.2 * torch.randn(D, device=DEV)).bfloat16(), (0.1 * torch.randn(D, device=DEV)).bfloat16()
+    y, out = torch.empty_like(x), torch.empty_like(x)
+    M, z = torch.zeros(B, H, 128, 128, device=DEV), torch.zeros(B, H, 128, device=DEV)
+    api.infini_attn_layer_norm_forward(x, w, b, y)
+    api.infini_attn_layer_forward(y, w_qkv, w_o, beta, M, z, out, H, N, DELTA)
+    torch.cuda.synchronize()
+    norm = torch.from_numpy(G.layer_norm(np64(x), np64(w), np64(b), 1e-5)).bfloat16()
+    wy, wM, _ = R.layer_forward(np64(norm), np64(w_qkv), np64(w_o), np64(beta), H, N, mode=DELTA, M0=np64(M) * 0, z0=np64(z) * 0)
+    got = np64(out)
+    assert np.abs(got - wy).max() <= 2e-2 * max(1.0, np.abs(wy).max())
+    assert np.linalg.norm(got - wy) <= 5e-3 * np.linalg.norm(wy)
+    assert np.linalg.norm(np64(M) - wM) <= 5e-3 * np.linalg.norm(wM)
