@@ -117,6 +117,7 @@ int segment_chunks(const Shape& s, long long chunks, bool bwd) {
 struct ChunkSpace {
   size_t T, P, vec, G, snap, dsnap, acc, segS, segD, segA, bytes;
   int seg;
+  bool split;
   ChunkSpace(const Shape& s, long long nc, bool bwd) {
     const size_t n = (size_t)s.B * s.H * nc, state = (size_t)col_warps(s.dv) * padded_dk(s.dk) * 16 * 4;
     size_t at = 0;
@@ -131,7 +132,10 @@ struct ChunkSpace {
     G = take(n * kC * 8);
     snap = take(bwd ? n * state : 0);
     dsnap = take(bwd ? n * state : 0);
-    acc = take(bwd && s.H > s.Hk ? (size_t)s.B * s.Hk * nc * 2 * kC * padded_dk(s.dk) * 4 : 0);
+    // Few chunks: a block per value head (B 3, H 24, 6 key heads, L 20: the four heads of 18 blocks in turn take 159 us
+    // of the backward, side by side 80; with a block per SM and more already, the sum only costs).
+    split = bwd && s.H > s.Hk && (long long)s.B * s.Hk * nc < kSms;
+    acc = take(bwd && s.H > s.Hk ? (size_t)s.B * (split ? s.H : s.Hk) * nc * 2 * kC * padded_dk(s.dk) * 4 : 0);
     seg = segment_chunks(s, nc, bwd);
     const size_t nseg = (nc + seg - 1) / seg, m = nseg > 1 ? (size_t)s.B * s.H * nseg : 0;
     segS = take(m * state);
@@ -152,6 +156,7 @@ struct ChunkSpace {
     a.segD = reinterpret_cast<float4*>(w + segD);
     a.segA = reinterpret_cast<float4*>(w + segA);
     a.seg = seg;
+    a.split = split;
   }
 };
 
@@ -264,11 +269,15 @@ template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
   }
   if (rc == INFINI_OK) rc = run_both<T, DK, false>(a, nw, st);
   if (rc != INFINI_OK) return rc;
-  const dim3 chunks(a.nc, a.Hk, a.B);
+  const dim3 chunks(a.nc, a.split ? a.H : a.Hk, a.B);
   if constexpr (sizeof(T) == 2)
-    return GD_LAUNCH((grad_bf16_kernel<DK>), chunks, 512, sizeof(GradSmemB<DK>), kPhaseBwd, a, st);
+    rc = GD_LAUNCH((grad_bf16_kernel<DK>), chunks, 512, sizeof(GradSmemB<DK>), kPhaseBwd, a, st);
   else
-    return GD_LAUNCH((grad_kernel<T, DK>), chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
+    rc = GD_LAUNCH((grad_kernel<T, DK>), chunks, 256, sizeof(GradSmem<T, DK>), kPhaseBwd, a, st);
+  if (rc != INFINI_OK || !a.split) return rc;
+  LaunchScope scope(kPhaseBwd, st);
+  sum_heads_kernel<T, DK><<<dim3(a.nc, a.Hk, a.B), 256, 0, st>>>(a);
+  return launch_status();
 }
 
 // Sequences of fewer tokens than this go token by token (128 x 128, microseconds, tokens against a chunk of 64: bf16, 8

@@ -87,7 +87,10 @@ struct ChunkArgs {
   float* dg;
   float* dbeta;
   bool vec_dq, vec_dv;  // pairs of dq and dk, 16-byte rows of dv can be written whole
-  float* acc;  // grad, group > 1: [B Hk][nc][2][64][DK] running sums over the value heads of a key head
+  // grad, group > 1: dq and dk of one key head from its value heads, [B Hk][nc][2][64][DK] running sums of one block
+  // that takes them in turn, or (split) [B H][nc][2][64][DK] a block's own, which sum_heads_kernel adds
+  bool split;
+  float* acc;
 };
 
 // A sum of log decays as two floats, and e^(a - b) of two such sums where `in`, else 0.  The
@@ -998,7 +1001,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
   extern __shared__ __align__(16) uint8_t smem_raw[];
   GradSmem<T, DK>& s = *reinterpret_cast<GradSmem<T, DK>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
-  const int b = blockIdx.z, hk = blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int b = blockIdx.z, hk = a.split ? blockIdx.y / a.group : blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int h0 = a.split ? blockIdx.y : hk * a.group, heads = a.split ? 1 : a.group;
   const int i0 = blockIdx.x;
   const long long t0 = (long long)i0 * kC;
   const int n = chunk_len(row_len(a, b), i0);
@@ -1007,8 +1011,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
   T* dkk = static_cast<T*>(a.dkk) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
   const T zero = from_f32<T>(0.f);
   if (n == 0) {  // padding only
-    for (int x = tid; x < rows * a.dk; x += 256) dq[x] = dkk[x] = zero;
-    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
+    for (int x = tid; x < rows * a.dk && !a.split; x += 256) dq[x] = dkk[x] = zero;
+    for (int h = h0; h < h0 + heads; ++h) {
       const long long r0 = ((long long)b * a.H + h) * a.L + t0;
       for (int x = tid; x < rows * a.dv; x += 256) static_cast<T*>(a.dvv)[r0 * a.dv + x] = zero;
       if (tid < rows) a.dg[r0 + tid] = a.dbeta[r0 + tid] = 0.f;
@@ -1017,8 +1021,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
   }
   load_rows<T>(s.k, LD, static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[1] + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, 256);
   load_rows<T>(s.q, LD, static_cast<const T*>(a.q) + b * a.qs[0] + hk * a.qs[1] + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, 256);
-  for (int hi = 0; hi < a.group; ++hi) {
-    const int h = hk * a.group + hi;
+  for (int hi = 0; hi < heads; ++hi) {
+    const int h = h0 + hi;
     const long long bh = (long long)b * a.H + h, at = bh * a.nc + i0, r0 = bh * a.L + t0;
     load_rows<T>(s.d, LDD, static_cast<const T*>(a.d_out) + b * a.os[0] + h * a.os[1] + t0 * a.os[2], a.os[2], n, a.dv, 128, a.vec_o, tid, 256);
     load_tri_f32(s.Tm, a.T + at * 3 * kTri, tid, 256);
@@ -1305,7 +1309,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
           if (kk >= mt) mma2(K[mt][0], K[mt][1], kl[mt][0], kl[mt][1], load_a_m<PO>(s.P, kLdT, 16 * kk, 16 * mt, lane), bq);
         }
       }
-      float* acc = a.acc + (((long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
+      float* acc = a.acc + ((a.split ? bh : (long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -1322,7 +1326,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
                 const float2 oq = *pq, ok = *pk;
                 yq.x += oq.x; yq.y += oq.y; yk.x += ok.x; yk.y += ok.y;
               }
-              if (hi + 1 < a.group) {
+              if (a.split || hi + 1 < a.group) {
                 *pq = yq;
                 *pk = yk;
                 continue;
@@ -1393,7 +1397,8 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   GradSmemB<DK>& s = *reinterpret_cast<GradSmemB<DK>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c2 = 2 * (lane & 3);
-  const int b = blockIdx.z, hk = blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int b = blockIdx.z, hk = a.split ? blockIdx.y / a.group : blockIdx.y, nw = (a.dv + 15) >> 4;
+  const int h0 = a.split ? blockIdx.y : hk * a.group, heads = a.split ? 1 : a.group;
   const int i0 = blockIdx.x;
   const long long t0 = (long long)i0 * kC;
   const int n = chunk_len(row_len(a, b), i0);
@@ -1402,8 +1407,8 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
   bf16* dkk = static_cast<bf16*>(a.dkk) + (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
   const bf16 zero = from_f32<bf16>(0.f);
   if (n == 0) {  // padding only
-    for (int x = tid; x < rows * a.dk; x += 512) dq[x] = dkk[x] = zero;
-    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
+    for (int x = tid; x < rows * a.dk && !a.split; x += 512) dq[x] = dkk[x] = zero;
+    for (int h = h0; h < h0 + heads; ++h) {
       const long long r0 = ((long long)b * a.H + h) * a.L + t0;
       for (int x = tid; x < rows * a.dv; x += 512) static_cast<bf16*>(a.dvv)[r0 * a.dv + x] = zero;
       if (tid < rows) a.dg[r0 + tid] = a.dbeta[r0 + tid] = 0.f;
@@ -1414,8 +1419,8 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
   const int blks[2] = {half ? 1 : 0, half ? 2 : 3};
   load_rows<bf16>(s.k, LD, static_cast<const bf16*>(a.k) + b * a.ks[0] + hk * a.ks[1] + t0 * a.ks[2], a.ks[2], n, a.dk, DK, a.vec_k, tid, 512);
   load_rows<bf16>(s.q, LD, static_cast<const bf16*>(a.q) + b * a.qs[0] + hk * a.qs[1] + t0 * a.qs[2], a.qs[2], n, a.dk, DK, a.vec_k, tid, 512);
-  for (int hi = 0; hi < a.group; ++hi) {
-    const int h = hk * a.group + hi;
+  for (int hi = 0; hi < heads; ++hi) {
+    const int h = h0 + hi;
     const long long bh = (long long)b * a.H + h, at = bh * a.nc + i0, r0 = bh * a.L + t0;
     load_rows<bf16>(s.d, kLdG, static_cast<const bf16*>(a.d_out) + b * a.os[0] + h * a.os[1] + t0 * a.os[2], a.os[2], n, a.dv, 128, a.vec_o, tid, 512);
     load_rows<bf16>(s.M, kLdG, static_cast<const bf16*>(a.v) + b * a.vs[0] + h * a.vs[1] + t0 * a.vs[2], a.vs[2], n, a.dv, 128, a.vec_v, tid, 512);
@@ -1756,7 +1761,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
           if (kk >= mt) mma2(K[x][0], K[x][1], load_tri_a_m<2>(s.P, kk, mt, lane), bq);
         }
       }
-      float* acc = a.acc + (((long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
+      float* acc = a.acc + ((a.split ? bh : (long long)b * a.Hk + hk) * a.nc + i0) * 2 * kC * DK;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -1772,7 +1777,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
                 const float2 oq = *pq, ok = *pk;
                 yq.x += oq.x; yq.y += oq.y; yk.x += ok.x; yk.y += ok.y;
               }
-              if (hi + 1 < a.group) {
+              if (a.split || hi + 1 < a.group) {
                 *pq = yq;
                 *pk = yk;
                 continue;
@@ -1798,6 +1803,35 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
           }
     }
     __syncthreads();
+  }
+}
+
+// dq and dk of a chunk from the value heads' own, in their order (split).
+template <typename T, int DK> __global__ void __launch_bounds__(256) sum_heads_kernel(const ChunkArgs a) {
+  const int b = blockIdx.z, hk = blockIdx.y, i0 = blockIdx.x;
+  const long long t0 = (long long)i0 * kC;
+  const int n = chunk_len(row_len(a, b), i0), rows = chunk_len(a.L, i0);
+  const long long out = (((long long)b * a.Hk + hk) * a.L + t0) * a.dk;
+  const float* acc = a.acc + (((long long)b * a.H + hk * a.group) * a.nc + i0) * 2 * kC * DK;
+#pragma unroll 2
+  for (int x = threadIdx.x; x < rows * (DK / 4); x += 256) {
+    const int t = x / (DK / 4), c = x % (DK / 4) * 4;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
+    if (t < n)
+#pragma unroll 4
+      for (int hi = 0; hi < a.group; ++hi) {
+        const float* p = acc + (long long)hi * a.nc * 2 * kC * DK + t * DK + c;
+        const float4 u = *reinterpret_cast<const float4*>(p), w = *reinterpret_cast<const float4*>(p + kC * DK);
+        q.x += u.x; q.y += u.y; q.z += u.z; q.w += u.w;
+        k.x += w.x; k.y += w.y; k.z += w.z; k.w += w.w;
+      }
+    const float qs[4] = {q.x, q.y, q.z, q.w}, ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < a.dk) {
+        static_cast<T*>(a.dq)[out + (long long)t * a.dk + c + e] = from_f32<T>(qs[e]);
+        static_cast<T*>(a.dkk)[out + (long long)t * a.dk + c + e] = from_f32<T>(ks[e]);
+      }
   }
 }
 

@@ -272,6 +272,16 @@ def test_backward(B, H, Hk, L, dk, dv, t):
 
 
 @pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("group", [2, 3])
+def test_backward_many_chunks_of_shared_heads(group, t):
+    """Enough chunks that one block takes the value heads of a key head in turn."""
+    x, d_out, dS = backward_inputs(5, 4 * group, 4, 520, 48, 20, t, seed=group)
+    lens = torch.tensor([520, 64, 333, 0, 520], dtype=torch.int32, device=DEV)
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS, lens=lens)
+    check_backward(x, d_out, dS, got, lens=lens)
+
+
+@pytest.mark.parametrize("t", [BF, FP], ids=["bf16", "fp32"])
 def test_backward_lens(t):
     x, d_out, dS = backward_inputs(6, 4, 2, 200, 128, 48, t)
     lens = torch.tensor([0, 1, 64, 199, 300, -5], dtype=torch.int32, device=DEV)
