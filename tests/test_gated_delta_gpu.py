@@ -391,3 +391,31 @@ def test_long_sequences_of_few_heads(B, H, Hk, L, dk, dv, lens, t):
     check_backward(x, d_out, dS, got, lens=ln)
     got2 = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS, lens=ln)
     assert all(torch.equal(a, b) for a, b in zip(got, got2))
+
+
+def test_forward_in_slabs():
+    """More chunks than the workspace holds at once: the same as row by row, each of which fits."""
+    B, H, L = 8, 64, 8192
+    q, k, v, g, beta, _ = make(B, H, 8, L, 64, 32, decay=0.1)
+    assert api.infini_attn_gated_delta_workspace_size(B, H, 8, L, 64, 32) < api.infini_attn_gated_delta_workspace_size(1, H, 8, L, 64, 32) * B
+    lens = torch.tensor([8192, 1, 0, 64, 65, 5000, 8191, 4096], dtype=torch.int32, device=DEV)
+    S0 = torch.zeros(B, H, 64, 32, device=DEV)
+    out, S = forward(q, k, v, g, beta, S0, lens=lens)
+    for b, n in enumerate(lens.tolist()):
+        assert bool((out[b, :, n:] == 7.0).all())
+        if n:
+            o1, S1 = forward(*[y[b:b + 1, :, :n] for y in (q, k, v, g, beta)], S0[b:b + 1])
+            near(S[b:b + 1], np64(S1))
+            assert float((out[b, :, :n].float() - o1[0].float()).abs().max()) <= (TOL + 2 ** -7) * float(o1.abs().max())
+
+
+def test_state_pool_past_32_bits():
+    pool = 140000  # 2.29e9 elements
+    S = torch.empty(pool, 1, 128, 128, device=DEV)
+    S[-3:] = 0.1
+    q, k, v, g, beta, _ = make(2, 1, 1, 1, 128, 128)
+    one = [y[:, :, 0] for y in (q, k, v, g, beta)]
+    few, o1, o2 = S[-3:].clone(), torch.zeros(2, 1, 128, dtype=BF, device=DEV), torch.zeros(2, 1, 128, dtype=BF, device=DEV)
+    api.infini_attn_gated_delta_step(*one, S, o1, slots=torch.tensor([pool - 1, pool - 3], dtype=torch.int32, device=DEV))
+    api.infini_attn_gated_delta_step(*one, few, o2, slots=torch.tensor([2, 0], dtype=torch.int32, device=DEV))
+    assert torch.equal(S[-3:], few) and torch.equal(o1, o2)
