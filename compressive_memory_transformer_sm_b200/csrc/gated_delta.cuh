@@ -84,6 +84,11 @@ __global__ void __launch_bounds__(kRecurThreads) recur_kernel(const RecurArgs a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) vv[c] = col + c < a.dv ? to_f32(v[t * a.vs[2] + col + c]) : 0.f;
       __syncthreads();
+      if (decay == 0.f)  // cleared, and 0 * s would not be 0 of a state that is not finite
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
       float x[9] = {};  // kS and qS of four columns, q.k
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

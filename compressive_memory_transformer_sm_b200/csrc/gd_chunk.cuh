@@ -9,7 +9,9 @@
 // state from chunk to chunk.  Only differences G_i - G_j with i >= j enter an exponential, so
 // nothing overflows that the recurrence itself does not.  G is summed in 64 bits (a difference of
 // two sums near -100 would have lost 1e-5 in 32), from max(g, -1e4): e^-1e4 is 0 in fp32, and
-// differences stay finite where g is -inf.
+// differences stay finite where g is -inf.  A token whose own decay is 0 clears the state, one that
+// is not finite too: gamma is -0 (not 0) from that token on and Gamma in its chunk, and state_pass
+// selects there where 0 * S would not be 0.
 //
 // Gradients, with d denoting the loss's derivative and dS' that of the state after the chunk:
 //   dU = scale P^T dO + rho (K dS'),  dX = T^T dU,  dV = beta dX,  dA = -dX U^T,  dP = scale dO U^T
@@ -35,7 +37,7 @@ namespace gd {
 
 constexpr int kC = 64;             // tokens per chunk
 constexpr int kTri = 10 * 256;     // elements of a lower triangular 64 x 64 matrix: 16 x 16 blocks r >= c at r (r + 1) / 2 + c, swizzled (tri_at)
-constexpr int kVec = 256;          // floats per chunk: gamma[64], rho[64], beta[64], Gamma
+constexpr int kVec = 256;          // floats per chunk: gamma[64], rho[64], beta[64], Gamma; the sign of gamma, Gamma: cleared
 constexpr int kLdT = 68;           // leading dimension of 64 x 64 fp32 matrices in shared memory
 constexpr int kMaxWarps = 8;
 constexpr float kMinLog = -1e4f;
@@ -75,7 +77,8 @@ struct ChunkArgs {
   int seg, nseg;
   float4* segS;  // [B H][nseg][nw][DK / 8][32]: the state before a segment
   float4* segD;  // [B H][nseg][nw][DK / 8][32]: the gradient of the state after it
-  float4* segA;  // [B H][nseg][DK / 16][DK / 8][32]: A with S_after = A S_before + B, 16 columns of it per strip
+  float4* segA;  // [B H][nseg][DK / 16][DK / 8][32]: A with S_after = A S_before + B, 16 columns of it per strip; the first
+                 // segment has none, and there float i says whether segment i clears the state
   float* S;      // forward: [B, H, dk, dv], read and written
   void* out;
   const float* S0;  // bwd: initial values, may be null (zero)
@@ -251,11 +254,13 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
     const float* bp = a.beta + b * a.bs[0] + h * a.bs[1] + t0 * a.bs[2];
     double x[2];
     float be[2];
+    unsigned clear[2];  // bit l: token 2 l + i clears the state
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       const float gt = t < n ? gp[t * a.gs[2]] : 0.f;
       x[i] = gt < kMinLog ? kMinLog : gt;
+      clear[i] = __ballot_sync(0xffffffffu, expf(gt) == 0.f);
       be[i] = t < n ? bp[t * a.bs[2]] : 0.f;
     }
     double sum = x[0] + x[1];
@@ -272,10 +277,12 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
     s.beta[2 * lane + 1] = be[1];
     *reinterpret_cast<float4*>(a.G + at * kC + 2 * lane) = make_float4(two[0].x, two[0].y, two[1].x, two[1].y);
     float* v = a.vec + at * kVec;
-    *reinterpret_cast<float2*>(v + 2 * lane) = make_float2(expf((float)G0), expf((float)G1));
+    const unsigned before = (1u << lane) - 1, upto = (2u << lane) - 1;
+    const bool c0 = (clear[0] & upto) | (clear[1] & before), c1 = (clear[0] | clear[1]) & upto;
+    *reinterpret_cast<float2*>(v + 2 * lane) = make_float2(c0 ? -0.f : expf((float)G0), c1 ? -0.f : expf((float)G1));
     *reinterpret_cast<float2*>(v + 64 + 2 * lane) = make_float2(expf((float)(last - G0)), expf((float)(last - G1)));
     *reinterpret_cast<float2*>(v + 128 + 2 * lane) = make_float2(be[0], be[1]);
-    if (lane == 0) v[192] = expf((float)last);
+    if (lane == 0) v[192] = clear[0] | clear[1] ? -0.f : expf((float)last);
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -498,6 +505,7 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
       state_snap<ND>(S, before);
     }
   }
+  bool cleared = false;  // by a token of the segment
   fetch(0);
   for (int i = 0; i < nc; ++i) {
     if constexpr (KS > 1)
@@ -511,6 +519,8 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
     St& s = *reinterpret_cast<St*>(smem_raw + (a.stages == 2 ? i & 1 : 0) * stage);
     T* sv = reinterpret_cast<T*>(&s + 1);
     auto vec2 = [&](int which, int t) { return *reinterpret_cast<const float2*>(s.vec + 64 * which + 8 * t + c2); };
+    const float full = s.vec[192];
+    if (MODE == kPassSeg) cleared |= __float_as_uint(full) >> 31;
     if (live) {
       if (MODE == kPassSnap) state_snap<ND>(S, a.snap + (((bh * a.nc + first + i) * nw + wg) * (DK / 8) + ks * ND) * 32 + lane);
       // R^T = S^T K^T, Y^T = S^T Q^T
@@ -539,6 +549,30 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
               mma2(Y[x][0], Y[x][1], fo, fq);
           }
         }
+      }
+      if (__builtin_expect(__float_as_uint(full) >> 31, 0)) {
+        // A token of the chunk clears the state: a column of S that is not finite (every product with it is not) ends
+        // there.  The tokens before it have no answer; as zeros they leave nothing behind the clear, as they should.
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 gam = vec2(0, tile(x, y));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float gm = e & 1 ? gam.y : gam.x;
+              const bool after = __float_as_uint(gm) >> 31;
+              if (!isfinite(gm * (R[x][y][e] + lo[x][y][e]))) {
+                R[x][y][e] = lo[x][y][e] = 0.f;
+                if (OUT && !after) Y[x][y][e] = __int_as_float(0x7fffffff);
+              }
+              if (OUT && after && !isfinite(Y[x][y][e] + yl[x][y][e])) Y[x][y][e] = yl[x][y][e] = 0.f;
+            }
+          }
+#pragma unroll
+        for (int x = 0; x < ND; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[x][e] = 0.f;
       }
       // X^T = beta (V^T - gamma R^T), in R's place
 #pragma unroll
@@ -675,7 +709,6 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
         }
       }
       // S^T = Gamma S^T + (rho U)^T K
-      const float full = s.vec[192];
 #pragma unroll
       for (int np = 0; np < ND / 2; ++np) {
         float hi[2][4] = {}, lw[2][4] = {};
@@ -695,6 +728,8 @@ __device__ __forceinline__ void state_pass(const ChunkArgs& a, int vblock, int s
   }
   if (OUT && live && first + nc == all) state_store<ND>(S, a.S + bh * a.dk * a.dv, ks * DK / KS, v0, a.dk, a.dv, lane);
   if (MODE == kPassSeg && live) {
+    if (unit && wg == nw && ks == 0 && lane == 0)  // in segment 0's place, which no segment takes
+      reinterpret_cast<float*>(a.segA + bh * a.nseg * (DK / 16) * (DK / 8) * 32)[seg] = cleared ? 1.f : 0.f;
     if (unit)
       state_snap<ND>(S, a.segA + (((bh * a.nseg + seg) * (DK / 16) + wg - nw) * (DK / 8) + ks * ND) * 32 + lane);
     else if (seg + 1 < a.nseg)
@@ -915,8 +950,14 @@ template <int DK> __global__ void __launch_bounds__(128) combine_kernel(const Ch
   const float4* A = a.segA + bh * a.nseg * NS * (DK / 8) * 32 + lane;
   float S[ND][4];
   state_get<ND>(S, at + (back ? n - 2 : 1) * step);
+  // forward: the segments (32 at most) that clear the state
+  const unsigned clears = __ballot_sync(0xffffffffu, !back && lane > 0 && lane < n - 1 && reinterpret_cast<const float*>(A - lane)[lane] != 0.f);
   for (int k = 1; k < n - 1; ++k) {
     const int i = back ? n - 1 - k : k;  // the segment that is passed
+    if (clears >> i & 1) {  // A_i = 0, and S_i may not be finite
+      state_get<ND>(S, at + (i + 1) * step);
+      continue;
+    }
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < ND / 2; ++x) put_frag<3>(ex[warp * (ND / 2) + x][0], from_acc<3>(S[2 * x], S[2 * x + 1]), lane);

@@ -341,7 +341,10 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  * contiguous.  1 <= dk, dv <= 128.
  *
  * g is the logarithm of the decay, g <= 0 in use; -inf (or anything whose
- * exponential is 0) clears the state before the token.  Keys are used as they
+ * exponential is 0 in fp32) clears the state before the token, in the forward
+ * and the step also one that holds NaN or infinity.  (The backward takes finite
+ * states: of a chunk in which another is cleared, gradients may be NaN for the
+ * tokens behind the clear too.)  Keys are used as they
  * are given: the recurrence contracts while beta |k|^2 <= 2, which keys of
  * unit length and beta in [0, 2] meet.
  *
@@ -356,7 +359,7 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  * tokens, few long ones in segments side by side: the order of sums, and with
  * it the last bits, goes by B, H, L and the types, never by the data.  Inside a
  * chunk a NaN or infinity in k, v, g or beta also reaches the outputs of the
- * chunk's earlier tokens.
+ * chunk's earlier tokens, and passes a token of it that clears the state.
  *
  * The forward's workspace stays below about 1 GiB however long the sequences
  * are (it takes them in slabs).  The backward keeps the state and its gradient
