@@ -1394,7 +1394,11 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
 // ------------------------------------------------------------------ gradients, bf16
 // Bound by the tensor pipe and what feeds it: 26 thousand cycles of products in 54 thousand per chunk
 // and (b, h) (pipe active 48 %), at one block of 16 warps an SM for its 217 KB of operands.  4096
-// chunks in 893 us; with 8 warps that split the operands at each use 1770 us.
+// chunks in 934 us; with 8 warps that split the operands at each use 1770 us.  Products of order 2^-8
+// and below have sums of their own wherever dg and dbeta come from them (all orders in one sum: 902 us,
+// but dg and dbeta, relative to 64 bits, 4.9e-7 and 7.3e-7 instead of 3.0e-7 and 3.0e-7, which is what
+// the formulas in fp32 give); the sums of K S and Q S and those of K dS' one after the other, so that
+// they find room.
 // The same with 16 warps and every fp32 operand split once, where it is made: U and dX as three
 // planes [64][kLdG], T and P as they come, M + M^T and N as two.  Two warps share 16 value columns
 // (then 16 key columns): token blocks 0 and 3, or 1 and 2, so that the triangular products balance.
@@ -1412,7 +1416,7 @@ template <int DK> struct GradSmemB {
   float2 G[kC];
   float tok[8][3][kC];
   float rowP[10][16], colP[10][16], rowA[10][16], colA[10][16], rowB[10][16];
-  float sdot[8];
+  float sdot[16];
 };
 
 // Token sums of a warp's two blocks: x[block][tile][e] over the 16 value columns, to dst[64].
@@ -1482,31 +1486,78 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
       float R[2][2][4] = {}, Y[2][2][4] = {}, dot = 0.f;
       const float4* ps = snap + strip * (DK / 8) * 32 + lane;
       const float4* pd = dsnap + strip * (DK / 8) * 32 + lane;
-      float4 s0 = ps[0], s1 = ps[32], d0 = pd[0], d1 = pd[32];
+      {
+        float rl[2][2][4] = {}, yl[2][2][4] = {};
+        float4 s0 = ps[0], s1 = ps[32];
 #pragma unroll 1
-      for (int kk = 0; kk < DK / 16; ++kk) {
-        dot += s0.x * d0.x + s0.y * d0.y + s0.z * d0.z + s0.w * d0.w + s1.x * d1.x + s1.y * d1.y + s1.z * d1.z + s1.w * d1.w;
-        const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
-        const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
-        const AFrag<3> fs = from_acc<3>(sa, sb), fd = from_acc<3>(da, db);
-        if (kk + 1 < DK / 16) {
-          s0 = ps[(2 * kk + 2) * 32];
-          s1 = ps[(2 * kk + 3) * 32];
-          d0 = pd[(2 * kk + 2) * 32];
-          d1 = pd[(2 * kk + 3) * 32];
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          const float sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
+          const AFrag<3> fs = from_acc<3>(sa, sb);
+          if (kk + 1 < DK / 16) {
+            s0 = ps[(2 * kk + 2) * 32];
+            s1 = ps[(2 * kk + 3) * 32];
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            mma2(R[x][0], R[x][1], rl[x][0], rl[x][1], fs, load_b_k<1>(s.k, LD, 16 * blks[x], 16 * kk, lane));
+            mma2(Y[x][0], Y[x][1], yl[x][0], yl[x][1], fs, load_b_k<1>(s.q, LD, 16 * blks[x], 16 * kk, lane));
+          }
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const BFrag<1> bk = load_b_k<1>(s.k, LD, 16 * blks[x], 16 * kk, lane);
-          const BFrag<1> bq = load_b_k<1>(s.q, LD, 16 * blks[x], 16 * kk, lane);
-          mma2(R[x][0], R[x][1], fs, bk);
-          mma2(W[x][0], W[x][1], fd, bk);
-          mma2(Y[x][0], Y[x][1], fs, bq);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              R[x][t][e] += rl[x][t][e];
+              Y[x][t][e] += yl[x][t][e];
+            }
+      }
+      float lo[2][2][4] = {};
+      {
+        // two steps' loads in flight; S.dS' of every other step in each of the strip's two warps
+        float4 d[2][2], m[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          d[i][0] = pd[2 * i * 32];
+          d[i][1] = pd[(2 * i + 1) * 32];
+          m[i] = ps[(2 * half + i) * 32];
         }
+#pragma unroll 1
+        for (int k2 = 0; k2 < DK / 32; ++k2) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int kk = 2 * k2 + i;
+            const float4 d0 = d[i][0], d1 = d[i][1];
+            const float da[4] = {d0.x, d0.y, d0.z, d0.w}, db[4] = {d1.x, d1.y, d1.z, d1.w};
+            const AFrag<3> fd = from_acc<3>(da, db);
+            if (i == half)
+              dot += m[0].x * d0.x + m[0].y * d0.y + m[0].z * d0.z + m[0].w * d0.w + m[1].x * d1.x + m[1].y * d1.y + m[1].z * d1.z + m[1].w * d1.w;
+            if (k2 + 1 < DK / 32) {
+              d[i][0] = pd[(2 * kk + 4) * 32];
+              d[i][1] = pd[(2 * kk + 5) * 32];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              mma2(W[x][0], W[x][1], lo[x][0], lo[x][1], fd, load_b_k<1>(s.k, LD, 16 * blks[x], 16 * kk, lane));
+          }
+          if (k2 + 1 < DK / 32)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) m[i] = ps[(4 * k2 + 4 + 2 * half + i) * 32];
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              W[x][t][e] += lo[x][t][e];
+              lo[x][t][e] = 0.f;
+            }
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) s.sdot[strip] = dot;
+      if (lane == 0) s.sdot[warp] = dot;
       uint4* frag = reinterpret_cast<uint4*>(s.X) + strip * 4 * 3 * 32;
       const int v0 = 16 * strip + g;
       // sum_a = scale gamma dO.Y; then Y = V - gamma R (the error the write corrects), R stays K S
@@ -1537,13 +1588,18 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
         const AFrag<3> fx = get_frag<3>(frag + kk * 96, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (kk <= blks[x]) mma2(U[x][0], U[x][1], fx, load_tri_k<3>(s.Tm, blks[x], kk, lane));
+          if (kk <= blks[x]) mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fx, load_tri_k<3>(s.Tm, blks[x], kk, lane));
       }
       float sum[2][2][2];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            U[x][t][e] += lo[x][t][e];
+            lo[x][t][e] = 0.f;
+          }
           store_parts_t(s.U + (16 * blks[x] + 8 * t) * kLdG + 16 * strip, kPlaneG, kLdG, U[x][t], lane);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -1559,7 +1615,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
         const AFrag<1> fd = load_a_m<1>(s.d, kLdG, 16 * kk, 16 * strip, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (kk >= blks[x]) mma2(U[x][0], U[x][1], fd, load_tri_n<3>(s.P, kk, blks[x], lane));
+          if (kk >= blks[x]) mma2(U[x][0], U[x][1], lo[x][0], lo[x][1], fd, load_tri_n<3>(s.P, kk, blks[x], lane));
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -1567,8 +1623,8 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            U[x][t][e] = a.scale * U[x][t][e] + s.vec[64 + 16 * blks[x] + 8 * t + c2 + (e & 1)] * W[x][t][e];
-            W[x][t][e] = 0.f;
+            U[x][t][e] = a.scale * (U[x][t][e] + lo[x][t][e]) + s.vec[64 + 16 * blks[x] + 8 * t + c2 + (e & 1)] * W[x][t][e];
+            W[x][t][e] = lo[x][t][e] = 0.f;
           }
       named_bar_sync(1 + strip, 64);  // both warps have taken X
 #pragma unroll
@@ -1580,7 +1636,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
         const AFrag<3> fu = get_frag<3>(frag + kk * 96, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (kk >= blks[x]) mma2(W[x][0], W[x][1], fu, load_tri_n<3>(s.Tm, kk, blks[x], lane));
+          if (kk >= blks[x]) mma2(W[x][0], W[x][1], lo[x][0], lo[x][1], fu, load_tri_n<3>(s.Tm, kk, blks[x], lane));
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -1589,6 +1645,8 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int tk = 16 * blks[x] + 8 * t + c2 + e;
+            W[x][t][e] += lo[x][t][e];
+            W[x][t][2 + e] += lo[x][t][2 + e];
             sum_a[x][t][e] -= s.vec[128 + tk] * s.vec[tk] * (W[x][t][e] * R[x][t][e] + W[x][t][2 + e] * R[x][t][2 + e]);
             sum[x][t][e] = W[x][t][e] * Y[x][t][e] + W[x][t][2 + e] * Y[x][t][2 + e];
           }
@@ -1749,7 +1807,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) sum_e += __shfl_xor_sync(0xffffffffu, sum_e, o);
       float dot = 0.f;
-      for (int w = 0; w < nw; ++w) dot += s.sdot[w];
+      for (int w = 0; w < 2 * nw; ++w) dot += s.sdot[w];
       if (lane == 31) x[1] += sum_e + (double)s.vec[192] * dot;
       double sum = x[0] + x[1];
 #pragma unroll

@@ -168,6 +168,18 @@ def test_long_memories(H, kernels_of, t):
 
 
 @gpu
+def test_scalar_gradients_of_bf16_inputs():
+    """dg and dbeta are fp32 whatever the inputs' type.  They come from sums of 16 terms a step over 128 rows: 8 additions,
+    each truncating by 2^-24 of the sum in the mean, 8 * 2^-24 = 2^-21 if all have one sign.  (With the products of the
+    operands' low parts in the same sums it is 24 additions.)"""
+    x, d_out, dS = backward_inputs(1, 8, 8, 1024, 128, 128, BF, seed=45)
+    grads = reference(x, 128 ** -0.5, None, d_out, dS)[2]
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS)
+    for a, w in zip(got[3:5], grads[3:5]):
+        assert float((a.double() - w).norm() / w.norm()) <= 2.0 ** -21
+
+
+@gpu
 def test_slabs_of_segments():
     """More chunks than the workspace holds at once, of few enough heads that every slab is cut into segments."""
     B, H, L, dk, dv = 1, 40, 130000, 16, 16
