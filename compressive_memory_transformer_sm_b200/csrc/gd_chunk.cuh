@@ -45,7 +45,10 @@ constexpr float kMinLog = -1e4f;
 template <typename T, int DK> struct Dims {
   static constexpr int kLdK = DK + 16 / (int)sizeof(T);  // rows shifted by 4 banks
   static constexpr int kIn = sizeof(T) == 2 ? 1 : 3;     // parts of an input element
-  static constexpr int kOut = sizeof(T) == 2 ? 2 : 3;    // parts of an fp32 factor of a result that is rounded to T
+  // Parts of an fp32 factor of a result that is rounded to T.  For bf16 two: the error against 64 bits is that of the
+  // rounding, 1.66e-3, with two parts and with three (the results differ from the fp32 formulas' by 1.2e-4 and 4e-5),
+  // and three cost a tenth (B 4, H 32, L 4096: 684 us instead of 619; B 2, H 8, L 2048: 119 instead of 103).
+  static constexpr int kOut = sizeof(T) == 2 ? 2 : 3;
 };
 
 struct ChunkArgs {
