@@ -338,7 +338,8 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  * bf16 or (mode INFINI_F32) fp32, any strides of (B, head, L) with the last
  * dimension contiguous; all zero selects the contiguous layout.  g, beta
  * [B, H, L] fp32 with strides of their own; S [B, H, dk, dv] fp32,
- * contiguous.  1 <= dk, dv <= 128.
+ * contiguous.  1 <= dk, dv <= 128; B and L from 1 on (empty calls are refused,
+ * as by the rest of the library).
  *
  * g is the logarithm of the decay, g <= 0 in use; -inf (or anything whose
  * exponential is 0 in fp32) clears the state before the token, in the forward
@@ -367,8 +368,10 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  *
  * The forward's workspace stays below about 1 GiB however long the sequences
  * are (it takes them in slabs).  The backward keeps the state and its gradient
- * at every chunk: per token and value head 2 KB at 128 x 128, a little more
- * with the rest.
+ * at every chunk, and the chunk's matrices: at 128 x 128 per token 2.5 KB for
+ * every value head and, where value heads share key heads, 1 KB for every key
+ * head (with few chunks for every value head); for a chunk begun as for 64
+ * tokens.  infini_attn_gated_delta_backward_workspace_size has the exact figure.
  */
 typedef struct infini_attn_gated_delta_params {
   const void* q;
@@ -464,7 +467,7 @@ typedef struct infini_attn_gated_delta_step_params {
 INFINI_API int infini_attn_gated_delta_step(const infini_attn_gated_delta_step_params* p);
 
 /*
- * Layer normalisation of `rows` contiguous rows of D elements (1 <= D <= 16384):
+ * Layer normalisation of `rows` >= 1 contiguous rows of D elements (1 <= D <= 16384):
  * y = (x - mean) / sqrt(var + eps) * weight + bias.  x, y bf16 or (mode
  * INFINI_F32) fp32; weight, bias [D] bf16 or (INFINI_WEIGHT_F32) fp32; bias may
  * be NULL; y may be x.  fp32 arithmetic; y is rounded once.

@@ -85,6 +85,14 @@ def test_reference(lens):
         assert a.shape == w.shape and np.allclose(a.numpy(), w, rtol=1e-11, atol=1e-11, equal_nan=True)
 
 
+@pytest.mark.parametrize("B,H,Hk,per_head", [(1, 8, 8, 2552), (4, 32, 16, 2552 + 512), (4, 32, 8, 2552 + 256), (2, 4, 2, 2552 + 1024)])
+def test_backward_workspace(B, H, Hk, per_head):
+    """Per token and value head at 128 x 128: T and P in three parts, the scalars, two states a chunk; 1 KB a key head."""
+    L = 640 if B == 2 else 8192
+    for mode in (0, 0x10):
+        assert api.infini_attn_gated_delta_backward_workspace_size(B, H, Hk, L, 128, 128, mode) == per_head * B * H * L
+
+
 def check(name, got, want, live=None):
     if live is not None:
         got, want = torch.where(live, got, 0), torch.where(live, want, 0)
