@@ -282,7 +282,7 @@ template <typename T, int DK> int chunk_backward(ChunkArgs a, cudaStream_t st) {
 
 // Sequences of fewer tokens than this go token by token (128 x 128, microseconds, tokens against a chunk of 64: bf16, 8
 // heads, 20 tokens 13.4 / 13.8; 128 heads, 10 tokens 20.5 / 22.6, 16 tokens 30.7 / 22.6; fp32, 8 heads, 31 tokens
-// 19.3 / 22.2; 128 heads 57 / 72).
+// 19.3 / 22.2; 128 heads 57 / 72).  The switch lies between the 8 and the 128 heads that were measured.
 long long chunk_from(const Shape& s) {
   if (s.mode & INFINI_F32) return 36;
   return (long long)s.B * s.H <= kSms / 4 ? 20 : 11;

@@ -5,8 +5,8 @@
 //   (I + A) U = X,   A_ij = beta_i e^(G_i - G_j) k_i.k_j (i > j),   X = beta (V - gamma (K S))
 //   O  = scale (gamma (Q S) + P U),   P_ij = e^(G_i - G_j) q_i.k_j (i >= j)
 //   S' = Gamma S + K^T (rho U)
-// prep_kernel computes T = (I + A)^-1 and P of every chunk in parallel; state_kernel passes the
-// state from chunk to chunk.  Only differences G_i - G_j with i >= j enter an exponential, so
+// prep_kernel computes T = (I + A)^-1 and P of every chunk in parallel; state_pass (forward_kernel)
+// passes the state from chunk to chunk.  Only differences G_i - G_j with i >= j enter an exponential, so
 // nothing overflows that the recurrence itself does not.  G is summed in 64 bits (a difference of
 // two sums near -100 would have lost 1e-5 in 32), from max(g, -1e4): e^-1e4 is 0 in fp32, and
 // differences stay finite where g is -inf.  A token whose own decay is 0 clears the state, one that
@@ -20,8 +20,9 @@
 //   dbeta_i = dX_i.(V - gamma K S)_i + sum_j dA_ij e^(G_i-G_j) k_i.k_j
 //   dG collects every exponent's derivative; dg_t = sum_(i >= t) dG_i
 //   dS = Gamma dS' + scale Q^T (gamma dO) - K^T (beta gamma dX)
-// bwd_state_kernel passes dS from chunk to chunk, grad_kernel does the rest for all chunks in
-// parallel from the stored states and state gradients.
+// bwd_state_pass (both_kernel, beside state_pass) passes dS from chunk to chunk, grad_kernel or
+// grad_bf16_kernel does the rest for all chunks in parallel from the stored states and state
+// gradients.
 //
 // Every product runs on mma.sync with fp32 operands split into bf16 parts (gd_frag.cuh).  A group
 // of KS warps owns 16 columns of the state, transposed (rows = value columns): each warp holds
@@ -1780,7 +1781,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
       }
     }
     __syncthreads();
-    // ---- 3: dg, dbeta (warp 0, two tokens a lane); dQ and dK, 16 key columns and 32 tokens per warp
+    // ---- 3: dg, dbeta (warp 15, two tokens a lane); dQ and dK, 16 key columns and 32 tokens per warp
     if (warp == 15) {
       double x[2];
       double sum_e = 0.;
