@@ -94,7 +94,10 @@ double pass_time(double strips, double n) {
 }
 // Chunks per segment.  Segments run side by side, but all of them twice, and the first time with the unit vectors'
 // columns too: it pays where few (b, h) leave most SMs without work.  Measured at B 1, H 8, 512 chunks: forward 1174 us
-// in one piece, 820 in segments of 64; both passes of the backward, which fill the SMs better, 1403 and 1789.
+// in one piece, 820 in segments of 64; both passes of the backward, which fill the SMs better, 1403 and 1789.  For fp32 and
+// 64-row states the same model: whole calls in one piece and as it chooses, fp32 128 x 128, 8 heads x 32768 tokens 3399
+// and 2859, 1 x 4096 402 and 148; 64 x 64, 8 x 32768 1072 and 394 (bf16), 1729 and 771 (fp32), 16 x 16384 953 and 717;
+// backward fp32 128 x 128, 3 x 16384 2236 and 2194, 64 x 64, 8 x 8192 904 and 922 (the one of 44 where it lost).
 int segment_chunks(const Shape& s, long long chunks, bool bwd) {
   const double strips = (double)s.B * s.H * col_warps(s.dv), unit = (double)s.B * s.H * padded_dk(s.dk) / 16;
   const double whole = bwd ? 1.2 * pass_time(2 * strips, (double)chunks) : pass_time(strips, (double)chunks);
