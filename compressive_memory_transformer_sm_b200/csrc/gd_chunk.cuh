@@ -290,15 +290,18 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
   }
   cp_async_wait<0>();
   __syncthreads();
-  // warps 0-3: K K^T, warps 4-7: Q K^T, 16 rows each, column blocks up to the diagonal
+  // warps 0-3: K K^T, warps 4-7: Q K^T, 16 rows each, column blocks up to the diagonal.  The low orders of fp32 inputs
+  // in sums of their own: 48 truncated additions to one left 7e-7 of the outputs and gradients that come from T and P,
+  // 8 leave 2e-7 (one product has the same error from K S; the time is the same).
   const int rb = warp & 3, m0 = 16 * rb;
   const bool is_q = warp >= 4;
-  float acc[4][2][4] = {};
+  float acc[4][2][4] = {}, lo[4][2][4] = {};
   for (int kk = 0; kk < DK / 16; ++kk) {
     const AFrag<PI> fa = load_a_k<PI>(is_q ? s.q : s.k, LD, m0, 16 * kk, lane);
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
-      if (cb <= rb) mma2(acc[cb][0], acc[cb][1], fa, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
+      if (cb <= rb)
+        mma2(acc[cb][0], acc[cb][1], lo[cb][0], lo[cb][1], fa, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
   }
 #pragma unroll
   for (int cb = 0; cb < 4; ++cb)
@@ -312,7 +315,7 @@ template <typename T, int DK, int PP> __global__ void __launch_bounds__(256) pre
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool in = is_q ? i >= j + e : i > j + e;
-            x[e] = acc[cb][t][2 * e2 + e] * decay(s.G[i], s.G[j + e], in) * (is_q ? 1.f : s.beta[i]);
+            x[e] = (acc[cb][t][2 * e2 + e] + lo[cb][t][2 * e2 + e]) * decay(s.G[i], s.G[j + e], in) * (is_q ? 1.f : s.beta[i]);
           }
           if (is_q)
             put_parts<PP>(a.P + at * PP * kTri + tri_block(rb, cb) * 256 + tri_at(g + 8 * e2, 8 * t + c2), kTri, x[0], x[1]);
@@ -1211,6 +1214,23 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
       const int rb = warp & 3, m0 = 16 * rb;
       const bool is_a = warp >= 4;
       float acc[4][2][4] = {}, kk2[4][2][4] = {}, lo[4][2][4] = {};
+      if (is_a) {
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          const AFrag<PI> fk = load_a_k<PI>(s.k, LD, m0, 16 * kk, lane);
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb)
+            if (cb <= rb) mma2(kk2[cb][0], kk2[cb][1], lo[cb][0], lo[cb][1], fk, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
+        }
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              kk2[cb][t][e] += lo[cb][t][e];
+              lo[cb][t][e] = 0.f;
+            }
+      }
       for (int kk = 0; kk < nw; ++kk) {
         AFrag<3> fx;
         AFrag<PI> fd;
@@ -1228,13 +1248,6 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
               mma2(acc[cb][0], acc[cb][1], lo[cb][0], lo[cb][1], fd, fu);
           }
       }
-      if (is_a)
-        for (int kk = 0; kk < DK / 16; ++kk) {
-          const AFrag<PI> fk = load_a_k<PI>(s.k, LD, m0, 16 * kk, lane);
-#pragma unroll
-          for (int cb = 0; cb < 4; ++cb)
-            if (cb <= rb) mma2(kk2[cb][0], kk2[cb][1], fk, load_b_k<PI>(s.k, LD, 16 * cb, 16 * kk, lane));
-        }
       float row[2] = {}, rowb[2] = {};
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb)

@@ -356,7 +356,7 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  *
  * All sums are fp32 or better, and so is the state.  Fp32 results (S, dg, dbeta,
  * dS0, and everything with INFINI_F32) come from factors of 24 bits: relative
- * errors of 1e-7 to 8e-7 over a tensor.  Out, dq, dk and dv in bf16 are rounded
+ * errors of 1e-7 to 4e-7 over a tensor.  Out, dq, dk and dv in bf16 are rounded
  * once.  Short sequences are worked through token by token, longer ones in
  * chunks of 64 tokens, few long ones in segments side by side.  In chunks the
  * factors of a bf16 result keep 16 bits (a relative 2^-17 before the rounding,

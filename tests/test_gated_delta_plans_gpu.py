@@ -188,6 +188,19 @@ def test_scalar_gradients_of_bf16_inputs():
 
 
 @gpu
+@pytest.mark.parametrize("H,L", [(8, 1024), (40, 130)])
+def test_results_of_fp32_inputs(H, L):
+    """The bound of test_scalar_gradients_of_bf16_inputs for what comes from inputs of 24 bits; dk, the sum of four
+    products one after the other, twice that."""
+    x, d_out, dS = backward_inputs(1, H, H, L, 128, 128, FP, seed=46)
+    o, S, grads = reference(x, 128 ** -0.5, None, d_out, dS)
+    got = (*forward(*x), *api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS))
+    for name, a, w in zip(("out", "S", "dq", "dk", "dv", "dg", "dbeta", "dS0"), got, (o, S, *grads)):
+        err = float((a.double() - w).norm() / w.norm())
+        assert err <= 2.0 ** (-20 if name == "dk" else -21), f"{name}: {err:.2e}"
+
+
+@gpu
 def test_slabs_of_segments():
     """More chunks than the workspace holds at once, of few enough heads that every slab is cut into segments."""
     B, H, L, dk, dv = 1, 40, 130000, 16, 16
