@@ -443,7 +443,7 @@ template <int KS> __device__ __forceinline__ void group_sync(int group) {
 // K S -> X -> U -> S of each chunk on the tensor cores: per chunk and 16 value columns of a 128-row
 // state 692 products of 16 x 8 x 16 with outputs (192 K S, 128 Q S, 120 T X, 60 P U, 192 K^T U; blocks
 // above the diagonal are skipped), 8 cycles each on one of four sub-cores.  KS 1: 128 (b, h) x
-// 64 chunks in 520 us, the tensor pipe 52 % of the time active; two blocks to an SM, so that one's
+// 64 chunks in 520 us, the tensor pipe 48 % of the time active; two blocks to an SM, so that one's
 // loads and conversions run beside the other's products (one block of eight warps: 650 us, its warps
 // all do the same at the same time).  KS 4: 8 (b, h) x 512 chunks in 1170 us, 2.3 us a chunk, of
 // which products are 0.7 us; one warp per sub-core leaves every latency open.  Warps that only copy

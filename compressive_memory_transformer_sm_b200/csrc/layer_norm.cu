@@ -14,7 +14,7 @@
 //
 // Measured (bf16, of a 6544 GB/s copy): forward 32768 x 4096 98 us (84 %), 32768 x 1024 30 us (69 %);
 // backward 32768 x 4096 177 us (69 %), 32768 x 1024 55 us with its reduction (56 %; the issue slots
-// are two thirds busy with fp32 arithmetic and shuffles).  Odd rows: 32768 x 1025 57 and 111 us.
+// are 58 % busy with fp32 arithmetic and shuffles).  Odd rows: 32768 x 1025 57 and 111 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
