@@ -359,8 +359,8 @@ INFINI_API size_t infini_attn_backward_workspace_size(const infini_attn_bwd_para
  * errors of 1e-7 to 4e-7 over a tensor.  Out, dq, dk and dv in bf16 are rounded
  * once.  Short sequences are worked through token by token, longer ones in
  * chunks of 64 tokens, few long ones in segments side by side.  In chunks the
- * factors of a bf16 result keep 16 bits (a relative 2^-17 before the rounding,
- * which is 2^-9), so that about one element in two thousand is rounded to the
+ * factors of a bf16 result keep 16 bits (off by up to 2^-16 of a factor before a
+ * rounding of 2^-8), so that about one element in two thousand is rounded to the
  * other of its two neighbours.  The order of sums, and with it the last bits, goes by
  * B, H, L and the types, never by the data; results repeat bit for bit.  Inside a
  * chunk a NaN or infinity in k, v, g or beta also reaches the outputs of the

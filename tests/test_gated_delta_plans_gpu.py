@@ -7,8 +7,8 @@ Bounds.  Elementwise as in ``test_gated_delta_gpu``.  For fp32 results also rela
 most 8 steps of 16 terms, each of which may truncate the running sum by 2^-23 of it; truncations are spread evenly, so
 that their mean, which is what remains of them in a sum, is 2^-24 each: 8 * 2^-24 = 2^-21 a product if all have one
 sign.  A result is at the end of four products (K S, T X, K^T U and its own): 4 * 2^-21 = 2^-19 = 1.9e-6, and what
-earlier chunks left decays.  Operands of two bf16 parts instead of three (2^-17 of each, spread evenly: 2^-17 / sqrt(3)
-of those whose significand is 1, 2^-18 / sqrt(3) of those near 2, 3.2e-6 in the mean square) do not meet it."""
+earlier chunks left decays.  Values of two bf16 parts instead of three are off by up to 2^-8 of a remainder of up to
+2^-8, 2^-16 = 1.5e-5, and about 2.6e-6 in the mean square: X or rho U in two parts does not meet the bound."""
 
 import re
 
