@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kBlockThreads<TPR>) ln_backward_kernel(const A
     load_row<T, VEC, TPR, NV, SHIFT>(nd, a.dy, row + step, a, lane, off);
     float xs[NV][VEC];
     const float var = centre<T, VEC, TPR, NV, SHIFT>(cx, lane, a.D, off, xs, red, sub, RPB * NW);
-    const float rstd = 1.f / sqrtf(var + a.eps);
+    const float rstd = active ? 1.f / sqrtf(var + a.eps) : 0.f;  // 0 * (1 / 0) of a place without a row would reach dw
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

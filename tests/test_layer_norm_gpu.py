@@ -186,3 +186,14 @@ def test_norm_in_front_of_the_layer():
     assert np.abs(got - wy).max() <= 2e-2 * max(1.0, np.abs(wy).max())
     assert np.linalg.norm(got - wy) <= 5e-3 * np.linalg.norm(wy)
     assert np.linalg.norm(np64(M) - wM) <= 5e-3 * np.linalg.norm(wM)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(3, 64), (5, 100), (9, 256), (17, 512), (7, 1000), (1, 24)])
+def test_eps_zero(rows, D, t):
+    """Blocks hold several short rows at once: places without a row add nothing to the weights' gradients."""
+    x, w, b, dy = make(rows, D, t, torch.float32, 7 * rows + D)
+    y = torch.empty_like(x)
+    api.infini_attn_layer_norm_forward(x, w, b, y, eps=0.0)
+    check_forward(x, w, b, y, 0.0)
+    check_backward(x, w, dy, api.infini_attn_layer_norm_backward(x, w, dy, eps=0.0), 0.0)
