@@ -1029,6 +1029,24 @@ __device__ __forceinline__ void sum_rows(float (&x)[16], float* dst, int lane) {
     for (int i = 0; i < 16; ++i) dst[8 * (i >> 1) + 2 * lane + (i & 1)] = x[i];
 }
 
+// dg_t = sum over i >= t of x_i, the exponents' derivatives but for G_last - G_i's, and over i < t of these, e_i (all of
+// them count for G_last).  Two sums, and none of them a difference: e of the last token is as large as dv is whatever the
+// decays, dg e^g of that.  Tokens 2 lane, 2 lane + 1; `sum` is that of the x from 2 lane + 1 on, `before` that of the e
+// before 2 lane.
+__device__ __forceinline__ void decay_sums(const double (&x)[2], const double (&e)[2], double& sum, double& before, int lane) {
+  sum = x[0] + x[1];
+  before = e[0] + e[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_down_sync(0xffffffffu, sum, o), z = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane + o < 32) sum += y;
+    if (lane >= o) before += z;
+  }
+  const double y = __shfl_down_sync(0xffffffffu, sum, 1), z = __shfl_up_sync(0xffffffffu, before, 1);
+  sum = (lane < 31 ? y : 0.) + x[1];
+  before = lane > 0 ? z : 0.;
+}
+
 // B fragment [k = value column][n = key row] of the state whose accumulator-order copy of the
 // 16 value columns is p.
 template <int P> __device__ __forceinline__ BFrag<P> load_b_state(const float* p, int n0, int lane) {
@@ -1270,7 +1288,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
                 if (i >= jj) s.Tm[i * kLdT + jj] = m;
                 if (i > jj) s.Tm[jj * kLdT + i] = m;
               } else {
-                const float dp = a.scale * x, y = i >= jj ? dp * s.P[i * kLdT + jj] : 0.f;
+                const float dp = a.scale * x, y = i > jj ? dp * s.P[i * kLdT + jj] : 0.f;
                 row[e >> 1] += y;
                 col[e & 1] += y;
                 s.P[i * kLdT + jj] = dp * decay(s.G[i], s.G[jj], i >= jj);
@@ -1303,8 +1321,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
     __syncthreads();
     // ---- 3: dg, dbeta (warp 0, two tokens a lane); dQ and dK, 16 key columns per warp
     if (warp == 0) {
-      double x[2];
-      double sum_e = 0.;
+      double x[2], ev2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
@@ -1315,23 +1332,17 @@ template <typename T, int DK> __global__ void __launch_bounds__(256) grad_kernel
           bv += s.tok[w][2][t];
         }
         for (int w = 0; w < 8; ++w) cv += s.col[w][t];
-        x[i] = (double)av - ev + s.rowP[t] + s.rowA[t] - cv;
-        sum_e += ev;
+        x[i] = (double)av + s.rowP[t] + s.rowA[t] - cv;
+        ev2[i] = ev;
         if (t < rows) a.dbeta[r0 + t] = t < n ? bv + s.rowB[t] : 0.f;
       }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) sum_e += __shfl_xor_sync(0xffffffffu, sum_e, o);
       float dot = 0.f;
       for (int w = 0; w < nw; ++w) dot += s.sdot[w];
-      if (lane == 31) x[1] += sum_e + (double)s.vec[192] * dot;
-      double sum = x[0] + x[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += y;
-      }
-      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)sum : 0.f;
-      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum - x[0]) : 0.f;
+      if (lane == 31) x[1] += (double)s.vec[192] * dot;
+      double sum, before;
+      decay_sums(x, ev2, sum, before, lane);
+      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)(sum + x[0] + before) : 0.f;
+      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum + before + ev2[0]) : 0.f;
     }
     if (warp < DK / 16) {
       const int n0 = 16 * warp;
@@ -1760,7 +1771,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
               const float pe[2] = {(bf16_lo(p2) + bf16_lo(p1)) + bf16_lo(p0), (bf16_hi(p2) + bf16_hi(p1)) + bf16_hi(p0)};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float dp = a.scale * m[e], y = dec[e] != 0.f ? dp * pe[e] : 0.f;
+                const float dp = a.scale * m[e], y = i > j + e && dec[e] != 0.f ? dp * pe[e] : 0.f;
                 row[r] += y;
                 col[e] += y;
                 m[e] = dp * dec[e];
@@ -1796,8 +1807,7 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
     __syncthreads();
     // ---- 3: dg, dbeta (warp 15, two tokens a lane); dQ and dK, 16 key columns and 32 tokens per warp
     if (warp == 15) {
-      double x[2];
-      double sum_e = 0.;
+      double x[2], ev2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i, tb = t >> 4, tl = t & 15;
@@ -1817,23 +1827,17 @@ template <int DK> __global__ void __launch_bounds__(512) grad_bf16_kernel(const 
           bv += c <= tb ? x1 : 0.f;
           neg += c >= tb ? x2 : 0.f;
         }
-        x[i] = (double)av - ev + pos - neg;
-        sum_e += ev;
+        x[i] = (double)av + pos - neg;
+        ev2[i] = ev;
         if (t < rows) a.dbeta[r0 + t] = t < n ? bv : 0.f;
       }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) sum_e += __shfl_xor_sync(0xffffffffu, sum_e, o);
       float dot = 0.f;
       for (int w = 0; w < 2 * nw; ++w) dot += s.sdot[w];
-      if (lane == 31) x[1] += sum_e + (double)s.vec[192] * dot;
-      double sum = x[0] + x[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += y;
-      }
-      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)sum : 0.f;
-      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum - x[0]) : 0.f;
+      if (lane == 31) x[1] += (double)s.vec[192] * dot;
+      double sum, before;
+      decay_sums(x, ev2, sum, before, lane);
+      if (2 * lane < rows) a.dg[r0 + 2 * lane] = 2 * lane < n ? (float)(sum + x[0] + before) : 0.f;
+      if (2 * lane + 1 < rows) a.dg[r0 + 2 * lane + 1] = 2 * lane + 1 < n ? (float)(sum + before + ev2[0]) : 0.f;
     }
     if (strip < DK / 16) {
       const int n0 = 16 * strip;

@@ -201,6 +201,19 @@ def test_results_of_fp32_inputs(H, L):
 
 
 @gpu
+@types
+@pytest.mark.parametrize("g", [-6.0, -15.0, -30.0])
+def test_gradient_of_strong_decays(g, t):
+    """dg is e^g of what the other gradients are, and as near, by its own size."""
+    x, d_out, dS = backward_inputs(2, 4, 2, 150, 64, 48, t, seed=47)
+    x[3][:] = g * (1 + 0.1 * torch.rand(x[3].shape, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV))
+    grads = reference(x, 0.125, None, d_out, dS)[2]
+    got = api.infini_attn_gated_delta_backward(*x[:5], d_out, S0=x[5], dS_L=dS)
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), got, grads):
+        check(name, a, w)
+
+
+@gpu
 def test_slabs_of_segments():
     """More chunks than the workspace holds at once, of few enough heads that every slab is cut into segments."""
     B, H, L, dk, dv = 1, 40, 130000, 16, 16
